@@ -111,7 +111,7 @@ def draw(rng):
 # --------------------------------------------------------------- inputs --
 
 class _Held:
-    """A pool that goes with its state."""
+    """A pool that goes with the last of its state and of the page views that are outputs."""
 
     def __init__(self, pool):
         self.pool = pool
@@ -237,11 +237,12 @@ def prepare(case, seed):
                         max_context=max(c["P"], s.get("max_len", c["P"])),
                         query_heads=c["H"] * c.get("G", 1), window=c.get("window", 0),
                         differential=attn)
-        s["held"], s["pool"] = _Held(pool), pool
+        held, s["pool"] = _Held(pool), pool
         for i in range(c.get("L", 1)):
             k, v = pool.kv_pages(i)
             k.copy_(s["k"][i])
             v.copy_(s["v"][i])
+            k.held = v.held = held            # views of the pool's memory
             s["k"][i], s["v"][i] = k, v
         if attn:
             s["diff"] = pkv.Differential(s["lam"], norm_weight=s["weight"], norm_eps=EPS,
