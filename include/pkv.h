@@ -84,6 +84,10 @@ typedef enum pkv_dtype {
                                    applies (bf16 or fp32 storage, head_dim 64 or 128, 2 or
                                    more query heads per KV head) */
 
+#define PKV_POOL_DIFFERENTIAL 4u /* the pool's heads come in pairs and its requests carry the
+                                   scratch of the differential calls (pkv_differential);
+                                   kv_heads must be even.  Changes nothing else */
+
 /* bits of the device error word */
 #define PKV_DEVERR_SEQ_LEN 1u   /* a seq_len < 1, > max_seq_len, or needing > max_pages pages */
 #define PKV_DEVERR_PAGE_ID 2u   /* a page-table entry outside [0, pages) */
@@ -147,7 +151,8 @@ int pkv_pool_options_init(pkv_pool_options* options);
  *   seed:        free-list order: a FIFO queue initialised to a Fisher-Yates
  *                shuffle of 0..pages-1 driven by SplitMix64(seed), swap index
  *                next() mod (i + 1) for i = pages-1 down to 1.
- *   flags:       0, or PKV_POOL_HOST_ONLY and/or PKV_POOL_CUDA_CORES.
+ *   flags:       0, or any of PKV_POOL_HOST_ONLY, PKV_POOL_CUDA_CORES and
+ *                PKV_POOL_DIFFERENTIAL.
  * Supported by the kernels: head_dim a power of two, 2 <= head_dim <= 128 for
  * PKV_F32 and <= 256 for PKV_BF16 (else PKV_ERR_UNSUPPORTED, unless HOST_ONLY).
  * Equivalent to pkv_pool_create_ex with kv_heads = query_heads = heads.
@@ -221,6 +226,21 @@ int pkv_request_destroy(pkv_request* req);
  */
 int pkv_request_fork(const pkv_request* parent, pkv_request** child);
 
+/*
+ * Fork n children of `parent` at once (parallel samples or beams of one prompt):
+ * children[0 .. n) receive requests at the parent's visible length that share its
+ * full pages.  The partly filled last page, if there is one, is not shared: every
+ * child gets a private copy now -- one page each from the free list's front, in
+ * child order, K and V of all layers copied in one launch on `stream` (one for
+ * every 480 children) -- so that no child's first token has to copy it layer by
+ * layer.  Pages the parent leased ahead of its length are not shared.  Calls that
+ * use a child have to be ordered after that copy (the same stream).  All or
+ * nothing: BAD_STATE if the parent has a token pending, OUT_OF_PAGES if fewer
+ * than n pages are free and the length is not a whole number of pages.  n = 0 is
+ * allowed.
+ */
+int pkv_request_fork_batch(const pkv_request* parent, int n, pkv_request** children, void* stream);
+
 /* Number of requests referencing physical page `page` (0: free). */
 int pkv_pool_page_refs(const pkv_pool* pool, int32_t page, int* refs);
 
@@ -238,6 +258,36 @@ int pkv_lease_pages(pkv_request* req, int64_t n);
  * length to 0 and zero the counters ([SERVE-PAGED]; [CACHED-BIND] reset).
  * BAD_STATE while a token is pending. */
 int pkv_release_pages(pkv_request* req);
+
+/*
+ * Shorten the request to its first `length` positions (taking back rejected
+ * draft tokens): the pages past ceil(length / page_size), leased-ahead ones
+ * included, are dropped in logical order as pkv_release_pages drops them.  The
+ * counters keep what was done.  A page that stays and is shared is copied on the
+ * next write as always.  INVALID_ARGUMENT unless 0 <= length <= the visible
+ * length; BAD_STATE while a token is pending.
+ */
+int pkv_request_truncate(pkv_request* req, int64_t length);
+
+/*
+ * Keep n of the request's positions and forget the others (cache eviction): the
+ * kept rows of K and V move, in every layer, to positions 0 .. n-1 in the order of
+ * `keep`; the visible length becomes n.
+ *   keep   [n] int32, device: positions, each within [0, length), normally
+ *          ascending; n <= length
+ * Moves into ceil(n / page_size) pages leased from the free list's front, in one
+ * launch on `stream`; the request's references to its old pages (leased-ahead ones
+ * included) are then dropped as pkv_release_pages drops them, so shared pages stay
+ * with the requests that share them.  Work on pages that this call gives back has
+ * to be ordered after it (the same stream).  The rows behind position n - 1 of the
+ * last page are not written.  The counters keep what was done.  A position outside
+ * the length sets PKV_DEVERR_SEQ_LEN and its row is unspecified.  Keys keep
+ * whatever position encoding they carry.  On a host-only pool only the
+ * bookkeeping happens (`keep` is not read).  All or nothing: INVALID_ARGUMENT,
+ * OUT_OF_PAGES if too few pages are free beside the old ones, BAD_STATE while a
+ * token is pending.
+ */
+int pkv_request_compact(pkv_request* req, int64_t n, const int32_t* keep, void* stream);
 
 /* Visible (committed) length. */
 int pkv_request_length(const pkv_request* req, int64_t* visible_len);
@@ -513,12 +563,139 @@ int pkv_paged_prefill(pkv_pool* pool, int layer, int batch, int64_t total_new, c
                       const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
                       float* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------ differential attention -- */
+
+/*
+ * Differential attention: the difference of two softmax maps over one cache.  KV
+ * heads come in pairs (2p, 2p+1) and query heads in pairs (2i, 2i+1); query pair i
+ * reads KV pair p = i / (query_heads / kv_heads).  The pair's value row is both
+ * heads' side by side, V_j = [v_(2p),j | v_(2p+1),j], 2 head_dim wide.  With
+ *   A_m = softmax_j(q_(2i+m) . K_(2p+m),j / sqrt(head_dim)),  m = 0, 1,
+ *   d   = sum_j A_0,j V_j - lambda[i] sum_j A_1,j V_j,
+ * output head i (of query_heads / 2, each 2 head_dim wide) is
+ *   out = out_scale * norm_weight * d / sqrt(mean(d^2) + norm_eps)   (normalise != 0)
+ *   out = out_scale * d                                              (normalise == 0)
+ *   lambda       [query_heads / 2] fp32, device: the learned weight of the second
+ *                map (from its vectors, lambda = exp(lq1 . lk1) - exp(lq2 . lk2) +
+ *                lambda_init, taken once when the weights are loaded)
+ *   norm_weight  [2 head_dim] fp32, device, or NULL for ones; unused without the norm
+ *   norm_eps     > 0 when normalise != 0
+ *   out_scale    finite (1 - lambda_init in the usual block)
+ * The pool's layout, tables, appends, transactions and window are those of the
+ * plain calls; a request may mix both kinds of layer.  Needs a pool created with
+ * PKV_POOL_DIFFERENTIAL (else PKV_ERR_UNSUPPORTED).  PKV_POOL_CUDA_CORES does not
+ * concern these calls.  The struct is read during the call only; the arrays it
+ * points to must outlive the device work.
+ */
+typedef struct pkv_differential {
+    const float* lambda;
+    const float* norm_weight;
+    int normalise;
+    float norm_eps;
+    float out_scale;
+} pkv_differential;
+
+/* Device scratch bytes that pkv_paged_differential_decode needs. */
+int pkv_differential_workspace_size(const pkv_pool* pool, int batch, int64_t max_seq_len, size_t* bytes);
+
+/*
+ * pkv_paged_decode_attention with differential attention.  Same arguments, layout
+ * and append, with
+ *   seq_lens     a length of 0 is an empty slot of the batch: nothing is stored and
+ *                its rows of `out` are zeros
+ *   out          [batch][query_heads / 2][2 head_dim] fp32, device, 16-byte aligned
+ *   workspace    >= pkv_differential_workspace_size bytes, 16-byte aligned, contents
+ *                need no initialisation
+ * Both maps are taken in one pass: every K and V row is read once per KV pair.
+ * Results do not depend on the order in which the GPU runs the work.  Bad lengths
+ * or page ids set the pool's error word; the affected rows of `out` are then
+ * unspecified.  Enqueues two kernels on `stream` (split, merge) and returns without
+ * waiting; calls whose device work can overlap must use different workspaces.
+ */
+int pkv_paged_differential_decode(pkv_pool* pool, int layer, int batch, const float* q,
+                                  const void* k_new, const void* v_new, const int32_t* page_tables,
+                                  int max_pages, const int32_t* seq_lens, int64_t max_seq_len,
+                                  const pkv_differential* diff, float* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Device scratch bytes that pkv_paged_differential_prefill needs (0 when batch or
+ * total_new is 0). */
+int pkv_differential_prefill_workspace_size(const pkv_pool* pool, int batch, int64_t total_new,
+                                            size_t* bytes);
+
+/*
+ * pkv_paged_prefill with differential attention: same arguments, layout, append
+ * and causal rule (chunk token i of request b attends positions 0 .. L0_b + i, the
+ * last `window` of them), with
+ *   out          [total_new][query_heads / 2][2 head_dim] fp32, device, 16-byte aligned
+ *   workspace    >= pkv_differential_prefill_workspace_size bytes, 16-byte aligned
+ * A request with n_b = 0 appends nothing.  Bad lengths or page ids set the pool's
+ * error word; the affected rows are then unspecified, rows at or past
+ * cu_new[batch] are left as they were.
+ */
+int pkv_paged_differential_prefill(pkv_pool* pool, int layer, int batch, int64_t total_new,
+                                   const void* q, const void* k_new, const void* v_new,
+                                   const int32_t* cu_new, const int32_t* page_tables, int max_pages,
+                                   const int32_t* seq_lens, const pkv_differential* diff, float* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* pkv_append_and_attend with differential attention, for the pending token: out is
+ * [query_heads / 2][2 head_dim].  Same transaction, states and errors. */
+int pkv_append_and_attend_differential(pkv_request* req, int layer, const float* q, const void* k,
+                                       const void* v, const pkv_differential* diff, float* out,
+                                       void* stream);
+
+/* pkv_prefill_chunk with differential attention, for the pending chunk: out is
+ * [n][query_heads / 2][2 head_dim].  Same transaction, states and errors; the
+ * request's scratch grows to its largest chunk (a larger one than any before frees
+ * and reallocates it, which waits for the device). */
+int pkv_prefill_chunk_differential(pkv_request* req, int layer, const void* q, const void* k,
+                                   const void* v, const pkv_differential* diff, float* out,
+                                   void* stream);
+
+/* --------------------------------------------------------------- pages -- */
+
+/*
+ * Copy whole pages, K and V of every layer, in one launch: page dst_pages[i]
+ * becomes page src_pages[i], i < n.  A source may repeat; destinations must be
+ * distinct and none of them a source (else their contents are unspecified).
+ *   src_pages, dst_pages  [n] int32, device
+ * Stateless over bookkeeping: references, tables and the free list stay as they
+ * are.  An id outside [0, pages) sets PKV_DEVERR_PAGE_ID and its pair is skipped.
+ * Enqueues one kernel on `stream` and returns without waiting.
+ */
+int pkv_copy_pages(pkv_pool* pool, int n, const int32_t* src_pages, const int32_t* dst_pages,
+                   void* stream);
+
+/*
+ * Pack the kept rows of a batch of requests into new pages, K and V of every
+ * layer, in one launch.  Request b keeps the rows at positions
+ * keep[cu_keep[b]] .. keep[cu_keep[b+1] - 1] of its table; row i of them moves to
+ * position i of its new table, i.e. page new_tables[b][i / page_size], slot
+ * i % page_size.
+ *   keep         [total_keep] int32, device: positions in [0, seq_lens[b]), any order
+ *   cu_keep      [batch + 1] int32, device: cu_keep[0] = 0, non-decreasing,
+ *                cu_keep[batch] == total_keep
+ *   page_tables  [batch][max_pages] int32, device
+ *   seq_lens     [batch] int32, device: lengths before the call
+ *   new_tables   [batch][new_max_pages] int32, device; no page of it may be read by
+ *                the call (of any request)
+ * Slots behind a request's last kept row are left as they were.  Stateless over
+ * bookkeeping.  A position that fits neither its length nor a table sets
+ * PKV_DEVERR_SEQ_LEN, a page id outside the pool PKV_DEVERR_PAGE_ID; their rows
+ * are skipped.  Enqueues one kernel on `stream` and returns without waiting.
+ */
+int pkv_compact_pages(pkv_pool* pool, int batch, int64_t total_keep, const int32_t* keep,
+                      const int32_t* cu_keep, const int32_t* page_tables, int max_pages,
+                      const int32_t* seq_lens, const int32_t* new_tables, int new_max_pages,
+                      void* stream);
+
 /* ------------------------------------------------------------- tracing -- */
 
 /*
  * Kernel timing hook.  When `before` and `after` are non-NULL cudaEvent_t
  * handles, every later pkv_append_and_attend / pkv_paged_decode_attention /
- * pkv_paged_prefill on this pool records `before` on its stream immediately
+ * pkv_paged_prefill (and their differential forms) on this pool records `before` on its stream immediately
  * before the attention kernel and `after` immediately after it, so
  * cudaEventElapsedTime(before, after) is that kernel's device time.  NULL,
  * NULL turns the hook off.  The events stay owned by the caller.
@@ -537,10 +714,12 @@ int pkv_pool_set_timing_events(pkv_pool* pool, void* before, void* after);
  *   PKV_INJECT_NONE         disarm every hook.
  *   PKV_INJECT_LEASE        arg = n >= 1: the call that would take the n-th page
  *                           lease from now (pkv_lease_pages, pkv_begin_token,
- *                           pkv_begin_chunk; copy-on-write pages included) fails
+ *                           pkv_begin_chunk, copy-on-write pages included;
+ *                           pkv_request_fork_batch, pkv_request_compact) fails
  *                           with PKV_ERR_OUT_OF_PAGES and changes nothing.
  *   PKV_INJECT_LAYER        arg = layer: the next pkv_append_and_attend or
- *                           pkv_prefill_chunk on that layer that passes its
+ *                           pkv_prefill_chunk (or their differential forms)
+ *                           on that layer that passes its
  *                           argument and state checks fails with PKV_ERR_CUDA
  *                           before it enqueues anything; the layer stays not run.
  *   PKV_INJECT_DEVICE_WAIT  arg = split-kernel worker (0 .. workers - 1), device

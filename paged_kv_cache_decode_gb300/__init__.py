@@ -14,6 +14,12 @@ ABI without its ``pkv_`` prefix:
     paged_decode_attention(pool, layer, q, k_new, v_new, page_tables, seq_lens,
                            max_seq_len, out=out, workspace=ws)   # batched
 
+Differential attention (a pool made with differential=True) takes the learned
+weights as one object per layer:
+
+    diff = Differential(lam, norm_weight=w, norm_eps=1e-5, out_scale=0.8)
+    out = append_and_attend_differential(req, layer, q, k, v, diff)   # [H_q / 2, 2 d_h]
+
 The operations follow "Incremental Serving" (sections "Request flow" and
 "Paged KV-cache layout") and the attention arithmetic of "38 · Cached
 generation" (function incremental_mixture).
@@ -25,21 +31,24 @@ import ctypes
 import torch
 
 from .binding import (  # noqa: F401
-    lib, check, PkvError, pkv_counters, pkv_pool_options, LIB_PATH,
+    lib, check, PkvError, pkv_counters, pkv_differential, pkv_pool_options, LIB_PATH,
     PKV_OK, PKV_ERR_INVALID_ARGUMENT, PKV_ERR_OUT_OF_PAGES, PKV_ERR_CAPACITY_EXCEEDED,
     PKV_ERR_BAD_STATE, PKV_ERR_OUT_OF_MEMORY, PKV_ERR_CUDA, PKV_ERR_DEVICE_CHECK,
     PKV_ERR_NO_STORAGE, PKV_ERR_UNSUPPORTED, PKV_F32, PKV_BF16, PKV_POOL_HOST_ONLY,
-    PKV_POOL_CUDA_CORES,
+    PKV_POOL_CUDA_CORES, PKV_POOL_DIFFERENTIAL,
     PKV_DEVERR_SEQ_LEN, PKV_DEVERR_PAGE_ID, PKV_DEVERR_TIMEOUT, PKV_DEVERR_SHARED,
     PKV_INJECT_NONE, PKV_INJECT_LEASE, PKV_INJECT_LAYER, PKV_INJECT_DEVICE_WAIT,
 )
 
 __all__ = [
-    "Pool", "Request", "PkvError", "pool_create", "pool_destroy", "request_create",
+    "Pool", "Request", "Differential", "PkvError", "pool_create", "pool_destroy", "request_create",
     "request_destroy", "request_fork", "lease_pages", "release_pages", "begin_token", "append_and_attend",
     "commit_token", "abort_token", "begin_chunk", "prefill_chunk", "paged_decode_attention",
     "paged_decode_attention_shared",
     "paged_prefill", "workspace_size",
+    "request_fork_batch", "request_truncate", "request_compact", "copy_pages", "compact_pages",
+    "paged_differential_decode", "paged_differential_prefill", "append_and_attend_differential",
+    "prefill_chunk_differential",
     "check_device_status", "PKV_F32", "PKV_BF16",
 ]
 
@@ -84,17 +93,47 @@ class _DeviceArray:
                                          "data": (ptr, False), "version": 3, "strides": None}
 
 
+class Differential:
+    """One layer's learned weights of differential attention.
+
+    ``lam`` [query_heads / 2] fp32: the weight of each output head's second softmax map.
+    With ``normalise`` each output row (2 head_dim wide) is divided by its root mean
+    square (``norm_eps`` added to the mean) and multiplied by ``norm_weight`` (fp32,
+    None: ones); ``out_scale`` multiplies the result.  Holds the tensors."""
+
+    def __init__(self, lam, norm_weight=None, norm_eps: float = 1e-5, out_scale: float = 1.0,
+                 normalise: bool = True):
+        _dev(lam, "lam", torch.float32, (lam.numel(),))
+        if norm_weight is not None:
+            _dev(norm_weight, "norm_weight", torch.float32, (norm_weight.numel(),))
+        self.lam, self.norm_weight = lam, norm_weight
+        self._c = pkv_differential(lam.data_ptr(),
+                                   None if norm_weight is None else norm_weight.data_ptr(),
+                                   int(bool(normalise)), norm_eps, out_scale)
+
+    def _for(self, pool: "Pool"):
+        """The C struct, its sizes checked against the pool's heads."""
+        if self.lam.numel() != pool.query_heads // 2:
+            raise ValueError(f"lam must have {pool.query_heads // 2} elements, got {self.lam.numel()}")
+        if self.norm_weight is not None and self.norm_weight.numel() != 2 * pool.head_dim:
+            raise ValueError(f"norm_weight must have {2 * pool.head_dim} elements, "
+                             f"got {self.norm_weight.numel()}")
+        return ctypes.byref(self._c)
+
+
 class Pool:
     """A paged K/V pool: per layer, key and value pages [pages, heads, page_size, head_dim].
 
     ``heads`` is the number of KV heads stored per page; ``query_heads`` (default:
     ``heads``) the heads of the query and output, a multiple of ``heads``
     (grouped-query attention); ``window`` > 0 limits every query to the last
-    ``window`` positions (sliding window)."""
+    ``window`` positions (sliding window); ``differential`` pairs the heads for the
+    differential calls."""
 
     def __init__(self, layers: int, pages: int, heads: int, head_dim: int, page_size: int = 16,
                  dtype="f32", max_context: int = 4096, seed: int = 0, host_only: bool = False,
-                 query_heads: int = 0, cuda_cores: bool = False, window: int = 0):
+                 query_heads: int = 0, cuda_cores: bool = False, window: int = 0,
+                 differential: bool = False):
         self.layers, self.heads, self.head_dim, self.page_size = layers, heads, head_dim, page_size
         self.query_heads = query_heads or heads
         self.window = window
@@ -108,7 +147,8 @@ class Pool:
         o.head_dim, o.page_size, o.dtype, o.max_context = head_dim, page_size, self.dtype, max_context
         o.seed = seed & ((1 << 64) - 1)
         o.window = window
-        o.flags = (PKV_POOL_HOST_ONLY if host_only else 0) | (PKV_POOL_CUDA_CORES if cuda_cores else 0)
+        o.flags = ((PKV_POOL_HOST_ONLY if host_only else 0) | (PKV_POOL_CUDA_CORES if cuda_cores else 0)
+                   | (PKV_POOL_DIFFERENTIAL if differential else 0))
         h = ctypes.c_void_p()
         check(lib.pkv_pool_create_ex(ctypes.byref(o), ctypes.byref(h)), "pkv_pool_create_ex")
         self._h = h
@@ -292,6 +332,104 @@ class Pool:
             _stream_ptr(stream)), "pkv_paged_prefill")
         return out
 
+    # -- differential attention --------------------------------------------
+    def differential_workspace_size(self, batch: int, max_seq_len: int) -> int:
+        n = ctypes.c_size_t()
+        check(lib.pkv_differential_workspace_size(self.handle, batch, int(max_seq_len), ctypes.byref(n)),
+              "pkv_differential_workspace_size")
+        return n.value
+
+    def paged_differential_decode(self, layer: int, q, k_new, v_new, page_tables, seq_lens,
+                                  max_seq_len: int, diff: Differential, out=None, workspace=None,
+                                  stream=None):
+        """paged_decode_attention with differential attention: out [batch, query_heads / 2,
+        2 head_dim] fp32; a seq_lens entry of 0 is an empty slot (its rows are zeros)."""
+        B = q.shape[0]
+        H, HQ, D = self.heads, self.query_heads, self.head_dim
+        oshape = (B, HQ // 2, 2 * D)
+        if out is None:
+            out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            key = ("differential", B, max_seq_len)
+            if key not in self._ws:
+                n = self.differential_workspace_size(B, max_seq_len)
+                self._ws[key] = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+            workspace = self._ws[key]
+        if page_tables.dim() != 2 or page_tables.shape[0] != B:
+            raise ValueError("page_tables must be [batch, max_pages]")
+        check(lib.pkv_paged_differential_decode(
+            self.handle, layer, B,
+            _dev(q, "q", torch.float32, (B, HQ, D)),
+            _dev(k_new, "k_new", self.torch_dtype, (B, H, D)),
+            _dev(v_new, "v_new", self.torch_dtype, (B, H, D)),
+            _dev(page_tables, "page_tables", torch.int32, None), page_tables.shape[1],
+            _dev(seq_lens, "seq_lens", torch.int32, (B,)), int(max_seq_len), diff._for(self),
+            _dev(out, "out", torch.float32, oshape),
+            _dev(workspace, "workspace", torch.uint8, None), workspace.numel(),
+            _stream_ptr(stream)), "pkv_paged_differential_decode")
+        return out
+
+    def differential_prefill_workspace_size(self, batch: int, total_new: int) -> int:
+        n = ctypes.c_size_t()
+        check(lib.pkv_differential_prefill_workspace_size(self.handle, batch, total_new, ctypes.byref(n)),
+              "pkv_differential_prefill_workspace_size")
+        return n.value
+
+    def paged_differential_prefill(self, layer: int, q, k_new, v_new, cu_new, page_tables, seq_lens,
+                                   diff: Differential, out=None, workspace=None, stream=None):
+        """paged_prefill with differential attention: out [N, query_heads / 2, 2 head_dim] fp32."""
+        N = q.shape[0]
+        B = cu_new.shape[0] - 1
+        H, HQ, D = self.heads, self.query_heads, self.head_dim
+        oshape = (N, HQ // 2, 2 * D)
+        if out is None:
+            out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            key = ("differential_prefill", B, N)
+            if key not in self._ws:
+                n = self.differential_prefill_workspace_size(B, N)
+                self._ws[key] = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+            workspace = self._ws[key]
+        if page_tables.dim() != 2 or page_tables.shape[0] != B:
+            raise ValueError("page_tables must be [batch, max_pages]")
+        check(lib.pkv_paged_differential_prefill(
+            self.handle, layer, B, N,
+            _dev(q, "q", self.torch_dtype, (N, HQ, D)),
+            _dev(k_new, "k_new", self.torch_dtype, (N, H, D)),
+            _dev(v_new, "v_new", self.torch_dtype, (N, H, D)),
+            _dev(cu_new, "cu_new", torch.int32, (B + 1,)),
+            _dev(page_tables, "page_tables", torch.int32, None), page_tables.shape[1],
+            _dev(seq_lens, "seq_lens", torch.int32, (B,)), diff._for(self),
+            _dev(out, "out", torch.float32, oshape),
+            _dev(workspace, "workspace", torch.uint8, None), workspace.numel(),
+            _stream_ptr(stream)), "pkv_paged_differential_prefill")
+        return out
+
+    # -- pages -------------------------------------------------------------
+    def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
+        """Page dst_pages[i] becomes page src_pages[i], K and V of every layer (int32
+        tensors on the device; destinations distinct, none of them a source)."""
+        n = src_pages.numel()
+        check(lib.pkv_copy_pages(self.handle, n, _dev(src_pages, "src_pages", torch.int32, (n,)),
+                                 _dev(dst_pages, "dst_pages", torch.int32, (n,)), _stream_ptr(stream)),
+              "pkv_copy_pages")
+
+    def compact_pages(self, keep, cu_keep, page_tables, seq_lens, new_tables, stream=None) -> None:
+        """Pack the kept rows of every request into its new pages, K and V of every layer:
+        row keep[cu_keep[b] + i] of page_tables[b] moves to position i of new_tables[b]."""
+        B = cu_keep.shape[0] - 1
+        n = keep.numel()
+        for t, name in ((page_tables, "page_tables"), (new_tables, "new_tables")):
+            if t.dim() != 2 or t.shape[0] != B:
+                raise ValueError(f"{name} must be [batch, max_pages]")
+        check(lib.pkv_compact_pages(
+            self.handle, B, n, _dev(keep, "keep", torch.int32, (n,)),
+            _dev(cu_keep, "cu_keep", torch.int32, (B + 1,)),
+            _dev(page_tables, "page_tables", torch.int32, None), page_tables.shape[1],
+            _dev(seq_lens, "seq_lens", torch.int32, (B,)),
+            _dev(new_tables, "new_tables", torch.int32, None), new_tables.shape[1],
+            _stream_ptr(stream)), "pkv_compact_pages")
+
     def set_timing_events(self, before, after) -> None:
         """Record two torch.cuda.Event around every later split (attention) kernel
         launch of this pool; (None, None) turns it off."""
@@ -346,6 +484,7 @@ class Request:
 
     def __init__(self, pool: Pool, handle=None):
         self.pool = pool
+        self._chunk = 0         # rows of the last chunk begun
         if handle is None:
             handle = ctypes.c_void_p()
             check(lib.pkv_request_create(pool.handle, ctypes.byref(handle)), "pkv_request_create")
@@ -358,6 +497,32 @@ class Request:
         child = Request(self.pool, h)
         self.pool._requests.append(child)
         return child
+
+    def fork_batch(self, n: int, stream=None) -> list:
+        """n children that share this request's full pages; the partly filled last page is
+        copied for each of them at once."""
+        hs = (ctypes.c_void_p * max(n, 1))()
+        s = None if self.pool.host_only else _stream_ptr(stream)
+        check(lib.pkv_request_fork_batch(self.handle, n, hs, s), "pkv_request_fork_batch")
+        out = [Request(self.pool, ctypes.c_void_p(hs[i])) for i in range(n)]
+        self.pool._requests += out
+        return out
+
+    def truncate(self, length: int) -> None:
+        """Shorten to the first `length` positions; pages behind them are given back."""
+        check(lib.pkv_request_truncate(self.handle, length), "pkv_request_truncate")
+
+    def compact(self, keep, stream=None) -> None:
+        """Keep the positions in `keep` (int32 on the device, normally ascending) and forget
+        the others; they become positions 0 .. len(keep) - 1.  Host-only pools: the number
+        of positions kept, or a sequence of them."""
+        if self.pool.host_only:
+            n = keep if isinstance(keep, int) else len(keep)
+            check(lib.pkv_request_compact(self.handle, n, None, None), "pkv_request_compact")
+            return
+        n = keep.numel()
+        check(lib.pkv_request_compact(self.handle, n, _dev(keep, "keep", torch.int32, (n,)),
+                                      _stream_ptr(stream)), "pkv_request_compact")
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -415,6 +580,7 @@ class Request:
         """Open a chunk of n positions at the visible length; returns the first."""
         pos = ctypes.c_int64()
         check(lib.pkv_begin_chunk(self.handle, n, ctypes.byref(pos)), "pkv_begin_chunk")
+        self._chunk = n
         return pos.value
 
     def prefill_chunk(self, layer: int, q, k, v, out=None, stream=None):
@@ -430,6 +596,42 @@ class Request:
             self.handle, layer, _dev(q, "q", p.torch_dtype, qshape),
             _dev(k, "k", p.torch_dtype, kshape), _dev(v, "v", p.torch_dtype, kshape),
             _dev(out, "out", torch.float32, qshape), _stream_ptr(stream)), "pkv_prefill_chunk")
+        return out
+
+    def append_and_attend_differential(self, layer: int, q, k, v, diff: Differential, out=None,
+                                       stream=None):
+        """append_and_attend with differential attention; returns out [query_heads / 2,
+        2 d_h] fp32."""
+        p = self.pool
+        qshape = (p.query_heads, p.head_dim)
+        kshape = (p.heads, p.head_dim)
+        oshape = (p.query_heads // 2, 2 * p.head_dim)
+        if out is None:
+            out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+        check(lib.pkv_append_and_attend_differential(
+            self.handle, layer, _dev(q, "q", torch.float32, qshape),
+            _dev(k, "k", p.torch_dtype, kshape), _dev(v, "v", p.torch_dtype, kshape), diff._for(p),
+            _dev(out, "out", torch.float32, oshape), _stream_ptr(stream)),
+            "pkv_append_and_attend_differential")
+        return out
+
+    def prefill_chunk_differential(self, layer: int, q, k, v, diff: Differential, out=None, stream=None):
+        """prefill_chunk with differential attention; returns out [n, query_heads / 2, 2 d_h]
+        fp32."""
+        p = self.pool
+        n = q.shape[0]
+        if self._chunk and n != self._chunk:
+            raise ValueError(f"q holds {n} rows, the pending chunk {self._chunk}")
+        qshape = (n, p.query_heads, p.head_dim)
+        kshape = (n, p.heads, p.head_dim)
+        oshape = (n, p.query_heads // 2, 2 * p.head_dim)
+        if out is None:
+            out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+        check(lib.pkv_prefill_chunk_differential(
+            self.handle, layer, _dev(q, "q", p.torch_dtype, qshape),
+            _dev(k, "k", p.torch_dtype, kshape), _dev(v, "v", p.torch_dtype, kshape), diff._for(p),
+            _dev(out, "out", torch.float32, oshape), _stream_ptr(stream)),
+            "pkv_prefill_chunk_differential")
         return out
 
     def commit_token(self) -> None:
@@ -449,9 +651,10 @@ class Request:
 # --------------------------------------------------------- C-ABI names --
 
 def pool_create(layers, pages, heads, head_dim, page_size=16, dtype="f32", max_context=4096,
-                seed=0, host_only=False, query_heads=0, cuda_cores=False, window=0) -> Pool:
+                seed=0, host_only=False, query_heads=0, cuda_cores=False, window=0,
+                differential=False) -> Pool:
     return Pool(layers, pages, heads, head_dim, page_size, dtype, max_context, seed, host_only,
-                query_heads, cuda_cores, window)
+                query_heads, cuda_cores, window, differential)
 
 
 def pool_destroy(pool: Pool) -> None:
@@ -522,6 +725,46 @@ def paged_prefill(pool: Pool, layer, q, k_new, v_new, cu_new, page_tables, seq_l
                   workspace=None, stream=None):
     return pool.paged_prefill(layer, q, k_new, v_new, cu_new, page_tables, seq_lens, out,
                               workspace, stream)
+
+
+def request_fork_batch(parent: Request, n: int, stream=None) -> list:
+    return parent.fork_batch(n, stream)
+
+
+def request_truncate(req: Request, length: int) -> None:
+    req.truncate(length)
+
+
+def request_compact(req: Request, keep, stream=None) -> None:
+    req.compact(keep, stream)
+
+
+def copy_pages(pool: Pool, src_pages, dst_pages, stream=None) -> None:
+    pool.copy_pages(src_pages, dst_pages, stream)
+
+
+def compact_pages(pool: Pool, keep, cu_keep, page_tables, seq_lens, new_tables, stream=None) -> None:
+    pool.compact_pages(keep, cu_keep, page_tables, seq_lens, new_tables, stream)
+
+
+def paged_differential_decode(pool: Pool, layer, q, k_new, v_new, page_tables, seq_lens, max_seq_len,
+                              diff, out=None, workspace=None, stream=None):
+    return pool.paged_differential_decode(layer, q, k_new, v_new, page_tables, seq_lens, max_seq_len,
+                                          diff, out, workspace, stream)
+
+
+def paged_differential_prefill(pool: Pool, layer, q, k_new, v_new, cu_new, page_tables, seq_lens, diff,
+                               out=None, workspace=None, stream=None):
+    return pool.paged_differential_prefill(layer, q, k_new, v_new, cu_new, page_tables, seq_lens, diff,
+                                           out, workspace, stream)
+
+
+def append_and_attend_differential(req: Request, layer, q, k, v, diff, out=None, stream=None):
+    return req.append_and_attend_differential(layer, q, k, v, diff, out, stream)
+
+
+def prefill_chunk_differential(req: Request, layer, q, k, v, diff, out=None, stream=None):
+    return req.prefill_chunk_differential(layer, q, k, v, diff, out, stream)
 
 
 def check_device_status(pool: Pool) -> int:

@@ -29,6 +29,7 @@ PKV_F32 = 0
 PKV_BF16 = 1
 PKV_POOL_HOST_ONLY = 1
 PKV_POOL_CUDA_CORES = 2
+PKV_POOL_DIFFERENTIAL = 4
 
 PKV_DEVERR_SEQ_LEN = 1
 PKV_DEVERR_PAGE_ID = 2
@@ -54,6 +55,12 @@ class pkv_pool_options(ctypes.Structure):
 class pkv_counters(ctypes.Structure):
     _fields_ = [("committed_tokens", ctypes.c_int64), ("cache_appends", ctypes.c_int64),
                 ("score_cells", ctypes.c_int64)]
+
+
+class pkv_differential(ctypes.Structure):
+    _fields_ = [("lambda_", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
+                ("normalise", ctypes.c_int), ("norm_eps", ctypes.c_float),
+                ("out_scale", ctypes.c_float)]
 
 
 _i, _i64, _u64, _u32, _vp, _sz = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32,
@@ -97,6 +104,19 @@ SIGNATURES = {
     "pkv_workspace_size_shared": [_vp, _i, _i64, _i64, _P(_sz)],
     "pkv_paged_decode_attention_shared": [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64, _i64,
                                           _vp, _vp, _sz, _vp],
+    "pkv_request_fork_batch": [_vp, _i, _P(_vp), _vp],
+    "pkv_request_truncate": [_vp, _i64],
+    "pkv_request_compact": [_vp, _i64, _vp, _vp],
+    "pkv_differential_workspace_size": [_vp, _i, _i64, _P(_sz)],
+    "pkv_paged_differential_decode": [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64,
+                                      _P(pkv_differential), _vp, _vp, _sz, _vp],
+    "pkv_differential_prefill_workspace_size": [_vp, _i, _i64, _P(_sz)],
+    "pkv_paged_differential_prefill": [_vp, _i, _i, _i64, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                                       _P(pkv_differential), _vp, _vp, _sz, _vp],
+    "pkv_append_and_attend_differential": [_vp, _i, _vp, _vp, _vp, _P(pkv_differential), _vp, _vp],
+    "pkv_prefill_chunk_differential": [_vp, _i, _vp, _vp, _vp, _P(pkv_differential), _vp, _vp],
+    "pkv_copy_pages": [_vp, _i, _vp, _vp, _vp],
+    "pkv_compact_pages": [_vp, _i, _i64, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp],
     "pkv_pool_set_timing_events": [_vp, _vp, _vp],
     "pkv_pool_inject_fault": [_vp, _i, _i64, ctypes.c_uint64],
     "pkv_check_device_status": [_vp, _P(_u32)],

@@ -1,0 +1,1032 @@
+// Differential attention over the paged KV cache for sm_103a: decode of one new
+// token per request, and prefill of chunks through the same lanes.
+//
+// What is computed.  KV heads come in pairs (2p, 2p + 1) and query heads in pairs
+// (2i, 2i + 1); query pair i reads KV pair p = i / G.  Per pair, with the keys K of
+// head 2p (map 0) and of head 2p + 1 (map 1) and the values of both heads side by
+// side, V_j = [v_2p,j | v_2p+1,j] (2 d_h wide):
+//     A_m = softmax_j(q_(2i+m) . K_(2p+m),j / sqrt(d_h)),   m = 0, 1
+//     d   = sum_j A_0,j V_j - lambda_i sum_j A_1,j V_j
+//     out = s * w * d / sqrt(mean(d^2) + eps)       (without the norm: s * d)
+// Both maps run as online softmaxes over one pass of the cache: each K row is read
+// once for its map, each V row once for both maps.
+//
+// Work decomposition.  A lane is (request, KV pair, row block): up to R query rows
+// that share every key -- the G query pairs of a token, and in a prefill those of
+// several consecutive chunk tokens, each with its own causal end.  A lane's keys
+// are cut into tiles of 16 positions (one page holds whole tiles); all tiles of all
+// lanes are laid end to end and cut into W equal pieces, one per worker (a warp of
+// a grid that fills the GPU once), so that any mix of lengths is balanced to one
+// tile.  Every CTA derives the tile prefix from the lengths by itself: no plan
+// kernel runs first.  A lane inside one worker's piece is finished by it.  A lane
+// that crosses pieces leaves one partial (m, l, o) per row, map and worker in the
+// workspace; the merge kernel, launched as the split kernel's programmatic
+// dependent, joins them in worker order (no atomics: the same bits every time):
+//     o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s.
+//
+// Bound: the K and V bytes of the cache, read once (each query row adds 12 d_h
+// flops per key to the 8 d_h bytes (bf16) of a key's pair of K and V rows).
+//
+// Precision.  Scores, maxima, sums and accumulators are fp32; exponents are taken
+// in log2 units with log2(e) / sqrt(d_h) folded into q.
+//
+// Faults are not raised by trapping: bad lengths and page ids, and waits that run
+// out, set bits of the pool's device error word and the work is skipped.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "pkv.h"
+#include "pkv_internal.h"
+#include "ptx.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr uint64_t kWaitNs = 4000000000ull;     // 4 s per bounded wait
+constexpr int kPrefix = 1024;                   // entries of the tile prefix in shared memory
+constexpr int kRingBudget = 196608;             // stage-ring bytes of one CTA (one CTA per SM)
+
+struct DfParams {
+    const void* q;              // [token][2 * Hp * G][D], fp32 or (q_bf16) bf16
+    bool q_bf16;
+    const void* k_new;          // [B][2 * Hp][D] storage dtype; nullptr: rows are in the pages
+    const void* v_new;
+    void* k_pages;              // [pages][2 * Hp][P][D]
+    void* v_pages;
+    int64_t n_pages;
+    const int32_t* tables;
+    int max_pages;
+    const int32_t* table_rows;  // table row of request x; nullptr: x
+    const int32_t* seq_lens;    // nullptr: one request of length single_t
+    int single_t;
+    int64_t max_seq_len;
+    const int32_t* tok0;        // prefill blocks: first chunk row and token count of block x
+    const int32_t* ntok;        //   (nullptr: one token, row x)
+    int B, Hp, G, subs, P;      // subs: row blocks per (request, pair)
+    int64_t window;
+    float qscale;               // log2(e) / sqrt(D)
+    const float* lambda;        // [Hp * G]
+    const float* norm_weight;   // [2 D] or nullptr
+    int normalise;
+    float norm_eps, out_scale;
+    float* out;                 // [token][Hp * G][2 D]
+    int4* rec;                  // [W] lane that starts in worker w and ends after it:
+                                //   (request, pair * subs + sub, last worker, 1), or w = 0
+    float2* part_ml;            // [2 W][R][2]
+    float* part_o;              // [2 W][R][2][2 D]
+    int W, R;
+    unsigned* err;
+};
+
+__device__ __forceinline__ int len_at(const DfParams& p, int x) {
+    return p.seq_lens ? __ldg(p.seq_lens + x) : p.single_t;
+}
+
+__device__ __forceinline__ int ntok_at(const DfParams& p, int x) {
+    return p.ntok ? __ldg(p.ntok + x) : 1;
+}
+
+// First position any row of request x reads at length t: the window's first position
+// for its earliest token.
+__device__ __forceinline__ int first_pos(const DfParams& p, int t, int nt) {
+    if (p.window <= 0) return 0;
+    const int64_t s = (int64_t)t - (nt - 1) - p.window;
+    return s > 0 ? (int)s : 0;
+}
+
+__device__ __forceinline__ bool len_ok(const DfParams& p, int t) {
+    return t >= 0 && t <= p.max_seq_len && ((int64_t)t + p.P - 1) / p.P <= p.max_pages;
+}
+
+// Tiles of one lane of request x (0: an empty slot, or a length that is refused).
+__device__ __forceinline__ int tiles_at(const DfParams& p, int x) {
+    const int t = len_at(p, x);
+    if (t <= 0 || !len_ok(p, t)) return 0;
+    return (t + kTile - 1) / kTile - first_pos(p, t, ntok_at(p, x)) / kTile;
+}
+
+// Tile prefix over requests, every `stride` of them, in shared memory; all threads of
+// the CTA.  pre[e] = tiles of requests below e * stride; returns the total.
+struct Prefix {
+    int64_t pre[kPrefix + 1];
+    int64_t warp_sum[32];
+};
+
+__device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& entries) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int nw = nt >> 5;
+    stride = (p.B + kPrefix - 1) / kPrefix;
+    entries = (p.B + stride - 1) / stride;
+    const int per = (entries + nt - 1) / nt;            // entries of one thread
+    const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+    int64_t n = 0;
+    for (int x = e0 * stride; x < min(e1 * stride, p.B); ++x) {
+        n += tiles_at(p, x);
+        if (blockIdx.x == 0 && !len_ok(p, len_at(p, x))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+    }
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t at = incl - n, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) at += s.warp_sum[w];
+        total += s.warp_sum[w];
+    }
+    for (int e = e0; e < e1; ++e) {
+        s.pre[e] = at;
+        if (e + 1 < e1)
+            for (int x = e * stride; x < (e + 1) * stride; ++x) at += tiles_at(p, x);
+    }
+    if (tid == 0) s.pre[entries] = total;
+    __syncthreads();
+    return total;
+}
+
+// A place in the flattened (request, lane, tile) sequence.
+struct Cursor {
+    int x, ln, tile;            // request, lane of it, tile of the lane
+    int n, tile0, t;            // the request's tiles per lane, first tile, length
+};
+
+__device__ __forceinline__ void cursor_load(const DfParams& p, Cursor& c) {
+    c.t = len_at(p, c.x);
+    c.n = tiles_at(p, c.x);
+    c.tile0 = first_pos(p, c.t, ntok_at(p, c.x)) / kTile;
+}
+
+// Cursor at flattened tile f; *lane_start receives the flattened index of its lane.
+__device__ Cursor cursor_at(const DfParams& p, const Prefix& s, int stride, int entries, int64_t f) {
+    const int LN = p.Hp * p.subs;
+    int lo = 0, hi = entries - 1;               // largest e with LN * pre[e] <= f
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (LN * s.pre[mid] <= f) lo = mid;
+        else hi = mid - 1;
+    }
+    int64_t base = LN * s.pre[lo];
+    Cursor c;
+    c.x = lo * stride;
+    for (;;) {
+        const int n = tiles_at(p, c.x);
+        if (f < base + (int64_t)LN * n || c.x == p.B - 1) break;
+        base += (int64_t)LN * n;
+        ++c.x;
+    }
+    cursor_load(p, c);
+    const int64_t local = f - base;
+    c.ln = (int)(local / c.n);
+    c.tile = (int)(local - (int64_t)c.ln * c.n);
+    return c;
+}
+
+__device__ __forceinline__ void cursor_next(const DfParams& p, Cursor& c) {
+    if (++c.tile < c.n) return;
+    c.tile = 0;
+    if (++c.ln < p.Hp * p.subs) return;
+    c.ln = 0;
+    do {
+        ++c.x;
+    } while (c.x < p.B && tiles_at(p, c.x) == 0);
+    if (c.x < p.B) cursor_load(p, c);
+}
+
+// The rows of one lane: row r is query pair `head` of one token, at output row `row`
+// ([token][Hp * G]), attending positions start .. end - 1.
+struct LaneRows {
+    int t, nt, tok0, h, sub;
+};
+
+__device__ __forceinline__ LaneRows lane_rows(const DfParams& p, int x, int ln) {
+    LaneRows L;
+    L.t = len_at(p, x);
+    L.nt = ntok_at(p, x);
+    L.tok0 = p.tok0 ? __ldg(p.tok0 + x) : x;
+    L.h = ln / p.subs;
+    L.sub = ln - L.h * p.subs;
+    return L;
+}
+
+__device__ __forceinline__ bool row_at(const DfParams& p, const LaneRows& L, int r, int64_t& row,
+                                       int& head, int& start, int& end) {
+    const int idx = L.sub * p.R + r;
+    const bool ok = idx < L.nt * p.G;
+    const int tok = ok ? idx / p.G : 0;
+    head = L.h * p.G + (ok ? idx - tok * p.G : 0);
+    row = (int64_t)(L.tok0 + tok) * (p.Hp * p.G) + head;
+    end = ok ? L.t - (L.nt - 1 - tok) : 0;
+    start = (p.window > 0 && end > p.window) ? (int)(end - p.window) : 0;
+    return ok;
+}
+
+// ------------------------------------------------------- CUDA-core engine --
+
+// One warp's view of a tile: 16 rows of K and V of both heads of the pair, staged
+// by 1-D bulk copies as [K0 | K1 | Va | Vb], each 16 x D contiguous.  Lane l owns FPL
+// features of every row: partial dot products of 16 keys x 2 maps are reduced with a
+// transposed butterfly (31 shuffles per query row) that leaves lane l the score of
+// key l % 16 of map l / 16; the weights go through shared memory so that every lane
+// reads all 32 of a row with 8 broadcast loads, and V is read once for all rows and
+// both maps.
+template <typename T, int D, int R>
+struct CoreGeo {
+    static constexpr int ES = sizeof(T);
+    static constexpr int TB = kTile * D * ES;              // one head's rows of a tile
+    static constexpr int STAGE_BYTES = 4 * TB;
+    static constexpr int FIT = kRingBudget / (2 * STAGE_BYTES);
+    static constexpr int WARPS = FIT < 8 ? FIT : 8;
+    static constexpr int STAGES_FIT = kRingBudget / (WARPS * STAGE_BYTES);
+    static constexpr int STAGES = STAGES_FIT < 4 ? STAGES_FIT : 4;
+    static constexpr int FPL = D >= 32 ? D / 32 : 1;       // features of one lane
+    static constexpr int P_BYTES = R * 32 * 4;             // a warp's weights
+    static constexpr int SMEM = WARPS * (STAGES * (STAGE_BYTES + 16) + P_BYTES);
+    static_assert(WARPS >= 1 && STAGES >= 2 && SMEM <= 215 * 1024, "CTA does not fit an SM");
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_feats(const T* src, float* dst) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (N == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            dst[0] = v.x, dst[1] = v.y, dst[2] = v.z, dst[3] = v.w;
+        } else if constexpr (N == 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            dst[0] = v.x, dst[1] = v.y;
+        } else {
+            dst[0] = *src;
+        }
+    } else {
+        if constexpr (N == 1) {
+            dst[0] = __bfloat162float(*src);
+        } else {
+            uint32_t w[N / 2];
+            if constexpr (N == 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else if constexpr (N == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                w[0] = v.x, w[1] = v.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                dst[2 * i] = __uint_as_float(w[i] << 16);
+                dst[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(CoreGeo<T, D, R>::WARPS * 32, 1)
+differential_core_kernel(const __grid_constant__ DfParams p) {
+    using M = CoreGeo<T, D, R>;
+    constexpr int F = M::FPL;
+    pdl_launch_dependents();                    // the merge grid waits for this grid's end
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Prefix prefix;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = warp * gridDim.x + blockIdx.x;
+    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
+    float* pw = reinterpret_cast<float*>(after + warp * M::P_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after + M::WARPS * M::P_BYTES) + warp * M::STAGES;
+    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * (M::P_BYTES + M::STAGES * 8)) +
+                          warp * M::STAGES;
+    if (lane == 0) {
+        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+    }
+    int stride, entries;
+    const int64_t total = build_prefix(p, prefix, stride, entries);
+    const int LN = p.Hp * p.subs;
+
+    // empty slots: their rows of the output are zeros
+    for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
+        if (p.tok0 || tiles_at(p, x) > 0) continue;
+        float* o = p.out + (int64_t)x * p.Hp * p.G * 2 * D;
+        for (int i = threadIdx.x; i < p.Hp * p.G * 2 * D; i += blockDim.x) o[i] = 0.f;
+    }
+
+    const int64_t T_all = LN * total;
+    const int64_t We = T_all < p.W ? T_all : p.W;   // every worker that works has a tile
+    if (w >= We) return;
+    const int64_t begin = w * T_all / We, end = (w + 1) * T_all / We;
+    const int n_work = (int)(end - begin);
+    Cursor cur = cursor_at(p, prefix, stride, entries, begin);
+    Cursor prod = cur;
+    int64_t f = begin;                              // flattened index of cur
+    const uint64_t policy = l2_stream_policy();
+    const int tpp = p.P / kTile;
+
+    // lane i holds table entry tab_base + i of request tab_x
+    int tab_x = -1, tab_base = 0;
+    int32_t tab_val = -1;
+    auto issue = [&](int s) {
+        const int gt = prod.tile0 + prod.tile;
+        const int pi = gt / tpp;
+        if (prod.x != tab_x || pi < tab_base || pi >= tab_base + 32) {
+            tab_x = prod.x;
+            tab_base = pi;
+            const int e = pi + lane;
+            const int64_t row = p.table_rows ? __ldg(p.table_rows + tab_x) : tab_x;
+            tab_val = e < p.max_pages ? __ldg(p.tables + row * p.max_pages + e) : -1;
+        }
+        const int32_t page = __shfl_sync(0xffffffffu, tab_val, pi - tab_base);
+        if (lane == 0) {
+            stage_page[s] = page;
+            if (page < 0 || page >= p.n_pages) {
+                atomicOr(p.err, PKV_DEVERR_PAGE_ID);
+                mbar_arrive(&bars[s]);
+            } else {
+                const int h = prod.ln / p.subs;
+                const int64_t row = ((int64_t)page * 2 * p.Hp + 2 * h) * p.P + (gt - pi * tpp) * kTile;
+                const T* k = static_cast<const T*>(p.k_pages) + row * D;
+                const T* v = static_cast<const T*>(p.v_pages) + row * D;
+                unsigned char* dst = ring + s * M::STAGE_BYTES;
+                mbar_arrive_expect_tx(&bars[s], M::STAGE_BYTES);
+                bulk_copy_g2s(dst, k, M::TB, &bars[s], policy);
+                bulk_copy_g2s(dst + M::TB, k + (int64_t)p.P * D, M::TB, &bars[s], policy);
+                bulk_copy_g2s(dst + 2 * M::TB, v, M::TB, &bars[s], policy);
+                bulk_copy_g2s(dst + 3 * M::TB, v + (int64_t)p.P * D, M::TB, &bars[s], policy);
+            }
+        }
+        cursor_next(p, prod);
+    };
+    int issued = n_work < M::STAGES ? n_work : M::STAGES;
+    for (int s = 0; s < issued; ++s) issue(s);
+
+    const bool own = lane * F < D;                  // D < 32: the lanes past D idle
+    const int feat = own ? lane * F : 0;
+    const int key = lane & 15, half = lane >> 4;
+    float q[R][2][F], acc[R][2][2][F];
+    float m[R], l[R];                               // of this half's map
+    int r_start[R], r_end[R];
+    LaneRows L{};
+    bool has_start = false;
+    int s = 0;
+    uint32_t parity = 0;
+
+    for (int k = 0; k < n_work; ++k, ++f) {
+        if (k == 0 || cur.tile == 0) {              // a new lane piece
+            has_start = cur.tile == 0;
+            L = lane_rows(p, cur.x, cur.ln);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                int64_t row;
+                int head;
+                const bool ok = row_at(p, L, r, row, head, r_start[r], r_end[r]);
+#pragma unroll
+                for (int mm = 0; mm < 2; ++mm) {
+                    const int64_t at = (row * 2 + mm) * D + feat;
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        float x = 0.f;
+                        if (ok && own)
+                            x = p.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at + i])
+                                         : static_cast<const float*>(p.q)[at + i];
+                        q[r][mm][i] = x * p.qscale;
+                        acc[r][mm][0][i] = acc[r][mm][1][i] = 0.f;
+                    }
+                }
+                m[r] = -INFINITY;
+                l[r] = 0.f;
+            }
+        }
+        if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
+            if (lane == 0) {
+                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+                // copies of the other stages may still be in flight
+                for (int i = 1; i < M::STAGES && k + i < issued; ++i) {
+                    const int si = (s + i) % M::STAGES;
+                    mbar_wait_bounded(&bars[si], parity ^ (s + i >= M::STAGES ? 1u : 0u), kWaitNs);
+                }
+            }
+            return;
+        }
+        unsigned char* stage = ring + s * M::STAGE_BYTES;
+        T* rows = reinterpret_cast<T*>(stage);      // [K0 | K1 | Va | Vb][16][D]
+        const int gt = cur.tile0 + cur.tile, k0 = gt * kTile;
+        const int32_t page = stage_page[s];
+        if (page >= 0 && page < p.n_pages) {
+            const int lo = first_pos(p, L.t, L.nt);
+            const bool edge = k0 < lo || k0 + kTile > L.t;
+            if (edge) {
+                // rows that no query of the lane reads may hold anything: zeros, so that
+                // a weight of 0 times them is 0
+                for (int i = lane; i < kTile * 2 * D; i += 32) {
+                    const int row = (i / D) % kTile;
+                    if (k0 + row < lo || k0 + row >= L.t) rows[2 * kTile * D + i] = T(0.f);
+                }
+                __syncwarp();
+            }
+            if (p.k_new != nullptr && L.t - 1 >= k0 && L.t - 1 < k0 + kTile) {
+                // the new token's rows: into the staged tile and into the page
+                const int slot = L.t - 1 - k0;
+                const int64_t src = ((int64_t)cur.x * 2 * p.Hp + 2 * L.h) * D;
+                const int64_t dst =
+                    (((int64_t)page * 2 * p.Hp + 2 * L.h) * p.P + (L.t - 1) % p.P) * D;
+                for (int i = lane; i < 2 * D; i += 32) {
+                    const int hd = i / D, c = i - hd * D;
+                    const T kv = static_cast<const T*>(p.k_new)[src + i];
+                    const T vv = static_cast<const T*>(p.v_new)[src + i];
+                    rows[(hd * kTile + slot) * D + c] = kv;
+                    rows[((2 + hd) * kTile + slot) * D + c] = vv;
+                    if (L.sub == 0) {
+                        static_cast<T*>(p.k_pages)[dst + (int64_t)hd * p.P * D + c] = kv;
+                        static_cast<T*>(p.v_pages)[dst + (int64_t)hd * p.P * D + c] = vv;
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float v[32];                        // partial scores: 16 keys of map 0, of map 1
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float kf[F];
+                    load_feats<T, F>(rows + j * D + feat, kf);
+                    float x = q[r][j >> 4][0] * kf[0];
+#pragma unroll
+                    for (int i = 1; i < F; ++i) x = fmaf(q[r][j >> 4][i], kf[i], x);
+                    v[j] = own ? x : 0.f;
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) {
+                    const bool up = (lane & o) != 0;
+#pragma unroll
+                    for (int i = 0; i < o; ++i) {
+                        const float mine = up ? v[i + o] : v[i], other = up ? v[i] : v[i + o];
+                        v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+                    }
+                }
+                const float sc =
+                    (k0 + key >= r_start[r] && k0 + key < r_end[r]) ? v[0] : -INFINITY;
+                float mx = sc;
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float m_new = fmaxf(m[r], mx);
+                const float mb = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = exp2f(m[r] - mb);
+                const float pr = exp2f(sc - mb);
+                l[r] = fmaf(l[r], alpha, pr);
+                m[r] = m_new;
+                pw[r * 32 + lane] = pr;
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                    const float a0 = __shfl_sync(0xffffffffu, alpha, 0);
+                    const float a1 = __shfl_sync(0xffffffffu, alpha, 16);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int i = 0; i < F; ++i) {
+                            acc[r][0][hf][i] *= a0;
+                            acc[r][1][hf][i] *= a1;
+                        }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int kq = 0; kq < kTile; kq += 4) {
+                float4 w0[R], w1[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    w0[r] = *reinterpret_cast<const float4*>(pw + r * 32 + kq);
+                    w1[r] = *reinterpret_cast<const float4*>(pw + r * 32 + 16 + kq);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float va[F], vb[F];
+                    load_feats<T, F>(rows + (2 * kTile + kq + j) * D + feat, va);
+                    load_feats<T, F>(rows + (3 * kTile + kq + j) * D + feat, vb);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float x0 = (&w0[r].x)[j], x1 = (&w1[r].x)[j];
+#pragma unroll
+                        for (int i = 0; i < F; ++i) {
+                            acc[r][0][0][i] = fmaf(x0, va[i], acc[r][0][0][i]);
+                            acc[r][0][1][i] = fmaf(x0, vb[i], acc[r][0][1][i]);
+                            acc[r][1][0][i] = fmaf(x1, va[i], acc[r][1][0][i]);
+                            acc[r][1][1][i] = fmaf(x1, vb[i], acc[r][1][1][i]);
+                        }
+                    }
+                }
+            }
+        }
+        // the stage is free again: hand it to the copy engine
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (issued < n_work) {
+            issue(s);
+            ++issued;
+        }
+        if (++s == M::STAGES) {
+            s = 0;
+            parity ^= 1u;
+        }
+
+        const bool has_end = cur.tile == cur.n - 1;
+        if (has_end || k == n_work - 1) {           // the piece ends
+            const int slot = 2 * w + (has_start ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                int64_t row;
+                int head, st, en;
+                const bool ok = row_at(p, L, r, row, head, st, en);
+                float lt = l[r];
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+                if (has_start && has_end) {
+                    if (!ok) continue;
+                    const float l0 = __shfl_sync(0xffffffffu, lt, 0);
+                    const float l1 = __shfl_sync(0xffffffffu, lt, 16);
+                    const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
+                    const float i1 = l1 > 0.f ? __ldg(p.lambda + head) / l1 : 0.f;
+                    float d[2][F], sq = 0.f;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int i = 0; i < F; ++i) {
+                            d[hf][i] = acc[r][0][hf][i] * i0 - acc[r][1][hf][i] * i1;
+                            if (own) sq = fmaf(d[hf][i], d[hf][i], sq);
+                        }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    float c = p.out_scale;
+                    if (p.normalise) c *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
+                    if (own) {
+                        float* op = p.out + row * 2 * D + feat;
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int i = 0; i < F; ++i) {
+                                const int col = hf * D + i;
+                                const float nw =
+                                    p.norm_weight && p.normalise ? __ldg(p.norm_weight + feat + col) : 1.f;
+                                op[col] = d[hf][i] * c * nw;
+                            }
+                    }
+                } else {
+                    const int64_t at = ((int64_t)slot * R + r) * 2;
+                    if (key == 0) p.part_ml[at + half] = make_float2(m[r], lt);
+                    if (own) {
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                                for (int i = 0; i < F; ++i)
+                                    p.part_o[(at + mm) * 2 * D + hf * D + feat + i] = acc[r][mm][hf][i];
+                    }
+                }
+            }
+            if (has_start && !has_end && lane == 0) {
+                const int64_t lane_end = f - cur.tile + cur.n;
+                p.rec[w] = make_int4(cur.x, cur.ln, (int)((lane_end * We - 1) / T_all), 1);
+            }
+        }
+        cursor_next(p, cur);
+    }
+}
+
+// ------------------------------------------------------------------ merge --
+
+constexpr int kMergeThreads = 256;
+constexpr int kMaxWorkers = 2048;
+
+// CTA (w, r): joins row r of the lane that starts in worker w and ends in a later one
+// from the partials of its workers, then takes the difference and the norm.
+__global__ void __launch_bounds__(kMergeThreads) differential_merge_kernel(const DfParams p, int D) {
+    __shared__ float wgt[2][kMaxWorkers];
+    __shared__ float inv[2];
+    __shared__ float4 red[kMergeThreads];
+    __shared__ float sums[kMergeThreads / 32];
+    pdl_wait_primary();
+    const int w0 = blockIdx.x, r = blockIdx.y;
+    const int4 rc = p.rec[w0];
+    if (rc.w == 0) return;
+    const LaneRows L = lane_rows(p, rc.x, rc.y);
+    int64_t row;
+    int head, st, en;
+    if (!row_at(p, L, r, row, head, st, en)) return;
+    const int n = rc.z - w0 + 1;                    // pieces: slot 2 w0 + 1, then 2 (w0 + i)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto slot = [&](int i) { return (int64_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * p.R + r; };
+    if (warp < 2) {
+        float mx = -INFINITY;
+        for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.part_ml[slot(i) * 2 + warp].x);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mb = mx == -INFINITY ? 0.f : mx;
+        float lt = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = p.part_ml[slot(i) * 2 + warp];
+            const float x = exp2f(ml.x - mb);
+            wgt[warp][i] = x;
+            lt = fmaf(x, ml.y, lt);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+        if (lane == 0) inv[warp] = lt > 0.f ? 1.f / lt : 0.f;
+    }
+    __syncthreads();
+    // 2 maps x D / 2 vectors of 4 columns; the threads left over split the pieces
+    const int vecs = 2 * D / 4, lanes = 2 * vecs, groups = kMergeThreads / lanes;
+    const int g = tid / lanes, at = tid - g * lanes, mm = at / vecs, v = at - mm * vecs;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g < groups) {
+#pragma unroll 4
+        for (int i = g; i < n; i += groups) {
+            const float4 x =
+                __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(i) * 2 + mm) * 2 * D) + v);
+            const float c = wgt[mm][i];
+            a.x = fmaf(c, x.x, a.x), a.y = fmaf(c, x.y, a.y);
+            a.z = fmaf(c, x.z, a.z), a.w = fmaf(c, x.w, a.w);
+        }
+    }
+    red[tid] = a;
+    __syncthreads();
+    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sq = 0.f;
+    if (tid < vecs) {
+        float4 o[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            o[k] = red[k * vecs + tid];
+            for (int i = 1; i < groups; ++i) {
+                const float4 x = red[i * lanes + k * vecs + tid];
+                o[k].x += x.x, o[k].y += x.y, o[k].z += x.z, o[k].w += x.w;
+            }
+        }
+        const float i0 = inv[0], i1 = inv[1] * __ldg(p.lambda + head);
+        d.x = o[0].x * i0 - o[1].x * i1, d.y = o[0].y * i0 - o[1].y * i1;
+        d.z = o[0].z * i0 - o[1].z * i1, d.w = o[0].w * i0 - o[1].w * i1;
+        sq = d.x * d.x + d.y * d.y + d.z * d.z + d.w * d.w;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) sums[warp] = sq;
+    __syncthreads();
+    if (tid >= vecs) return;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeThreads / 32; ++i) t += sums[i];
+    float c = p.out_scale;
+    float4 nw = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (p.normalise) {
+        c *= 1.f / sqrtf(t / (2 * D) + p.norm_eps);
+        if (p.norm_weight) {
+            nw.x = __ldg(p.norm_weight + 4 * tid), nw.y = __ldg(p.norm_weight + 4 * tid + 1);
+            nw.z = __ldg(p.norm_weight + 4 * tid + 2), nw.w = __ldg(p.norm_weight + 4 * tid + 3);
+        }
+    }
+    reinterpret_cast<float4*>(p.out + row * 2 * D)[tid] =
+        make_float4(d.x * c * nw.x, d.y * c * nw.y, d.z * c * nw.z, d.w * c * nw.w);
+}
+
+// ----------------------------------------------------------- prefill lanes --
+
+struct ChunkParams {
+    int B, H, D, P, es, bt;         // bt: chunk tokens of one block
+    int64_t N, X, n_pages;
+    const int32_t* cu_new;          // nullptr: one request of N rows, length single_t
+    const int32_t* seq_lens;
+    int single_t;
+    const int32_t* tables;
+    int max_pages;
+    const void* k_new;
+    const void* v_new;
+    void* k_pages;
+    void* v_pages;
+    int32_t *rows, *lens, *tok0, *ntok, *first;
+    unsigned* err;
+};
+
+__device__ __forceinline__ int chunk_cu(const ChunkParams& p, int b) {
+    return p.cu_new ? __ldg(p.cu_new + b) : (b == 0 ? 0 : (int)p.N);
+}
+
+__device__ __forceinline__ int64_t chunk_len(const ChunkParams& p, int b) {
+    return p.seq_lens ? __ldg(p.seq_lens + b) : p.single_t;
+}
+
+__device__ __forceinline__ bool chunk_ok(const ChunkParams& p, int b) {
+    const int64_t c0 = chunk_cu(p, b), c1 = chunk_cu(p, b + 1), t = chunk_len(p, b);
+    return c0 >= 0 && c1 >= c0 && c1 <= p.N && t - (c1 - c0) >= 0 && t <= (int64_t)p.max_pages * p.P;
+}
+
+// Every new key / value row into its page: VEC bytes a thread.
+template <int VEC>
+__global__ void __launch_bounds__(256) differential_append_kernel(const ChunkParams p) {
+    const int pieces = p.D * p.es / VEC;
+    const int64_t total = p.N * p.H * pieces;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t x = i / (p.H * pieces);
+        const int rem = (int)(i - x * p.H * pieces);
+        const int h = rem / pieces, u = rem - h * pieces;
+        int lo = 0, hi = p.B;                       // last request with cu_new[b] <= x
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (chunk_cu(p, mid) <= x) lo = mid;
+            else hi = mid;
+        }
+        if (!chunk_ok(p, lo)) continue;             // the plan reports it
+        const int64_t c0 = chunk_cu(p, lo), c1 = chunk_cu(p, lo + 1);
+        if (x < c0 || x >= c1) continue;
+        const int64_t pos = chunk_len(p, lo) - (c1 - c0) + (x - c0);
+        const int32_t page = p.tables[(int64_t)lo * p.max_pages + pos / p.P];
+        if (page < 0 || page >= p.n_pages) {
+            atomicOr(p.err, PKV_DEVERR_PAGE_ID);
+            continue;
+        }
+        const int64_t dst = ((((int64_t)page * p.H + h) * p.P + pos % p.P) * p.D) * p.es + (int64_t)u * VEC;
+        const int64_t src = ((x * p.H + h) * p.D) * p.es + (int64_t)u * VEC;
+        const char *ks = static_cast<const char*>(p.k_new) + src, *vs = static_cast<const char*>(p.v_new) + src;
+        char *kd = static_cast<char*>(p.k_pages) + dst, *vd = static_cast<char*>(p.v_pages) + dst;
+        if constexpr (VEC == 16) {
+            *reinterpret_cast<uint4*>(kd) = *reinterpret_cast<const uint4*>(ks);
+            *reinterpret_cast<uint4*>(vd) = *reinterpret_cast<const uint4*>(vs);
+        } else {
+            *reinterpret_cast<uint32_t*>(kd) = *reinterpret_cast<const uint32_t*>(ks);
+            *reinterpret_cast<uint32_t*>(vd) = *reinterpret_cast<const uint32_t*>(vs);
+        }
+    }
+}
+
+// Blocks of bt chunk tokens, request by request: table row, length after the block's
+// last token, first chunk row, tokens.  Blocks past the last have length 0.  One CTA.
+__global__ void __launch_bounds__(1024) differential_blocks_kernel(const ChunkParams p) {
+    __shared__ int warp_sum[32];
+    __shared__ int carry_s;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    if (tid == 0) carry_s = 0;
+    __syncthreads();
+    for (int base = 0; base < p.B; base += 1024) {
+        const int b = base + tid;
+        int nb = 0;
+        if (b < p.B) {
+            if (!chunk_ok(p, b)) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+            else nb = (chunk_cu(p, b + 1) - chunk_cu(p, b) + p.bt - 1) / p.bt;
+        }
+        int incl = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_sum[wid] = incl;
+        __syncthreads();
+        int at = carry_s + incl - nb, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < wid) at += warp_sum[w];
+            all += warp_sum[w];
+        }
+        if (b < p.B) p.first[b] = at;
+        __syncthreads();
+        if (tid == 0) carry_s += all;
+        __syncthreads();
+    }
+    const int total = carry_s;
+    // requests whose row ranges overlap can hold more blocks than the launch has room for
+    if (total > p.X && tid == 0) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+    for (int64_t x = tid; x < p.X; x += 1024) {
+        int row = 0, len = 0, t0 = 0, nt = 0;
+        if (x < total) {
+            int lo = 0, hi = p.B;                   // last request with first[b] <= x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.first[mid] <= x) lo = mid;
+                else hi = mid;
+            }
+            const int c0 = chunk_cu(p, lo), n = chunk_cu(p, lo + 1) - c0;
+            const int k = (int)(x - p.first[lo]) * p.bt;
+            row = lo;
+            t0 = c0 + k;
+            nt = n - k < p.bt ? n - k : p.bt;
+            len = (int)(chunk_len(p, lo) - n + k + nt);
+        }
+        p.rows[x] = row;
+        p.lens[x] = len;
+        p.tok0[x] = t0;
+        p.ntok[x] = nt;
+    }
+}
+
+// ------------------------------------------------------------------- host --
+
+// Opt a kernel into its dynamic shared memory, once per device.
+template <typename K>
+cudaError_t configure(K kernel, int bytes, bool* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+// Rows of one lane for G query pairs per KV pair.
+int core_rows(int dtype, int D, int G) {
+    if (D != 64 && D != 128) return 1;
+    return G >= 4 ? 4 : G;
+}
+
+// All instantiations: f(T, D, R).
+#define PKV_DF_CORE(F)                                                                    \
+    F(float, 2, 1) F(float, 4, 1) F(float, 8, 1) F(float, 16, 1) F(float, 32, 1)           \
+    F(float, 64, 1) F(float, 64, 2) F(float, 64, 4)                                       \
+    F(float, 128, 1) F(float, 128, 2) F(float, 128, 4)                                    \
+    F(__nv_bfloat16, 2, 1) F(__nv_bfloat16, 4, 1) F(__nv_bfloat16, 8, 1)                  \
+    F(__nv_bfloat16, 16, 1) F(__nv_bfloat16, 32, 1) F(__nv_bfloat16, 256, 1)              \
+    F(__nv_bfloat16, 64, 1) F(__nv_bfloat16, 64, 2) F(__nv_bfloat16, 64, 4)               \
+    F(__nv_bfloat16, 128, 1) F(__nv_bfloat16, 128, 2) F(__nv_bfloat16, 128, 4)
+
+template <typename T, int D, int R>
+cudaError_t launch_core(const DfParams& p, int sms, cudaStream_t stream) {
+    using M = CoreGeo<T, D, R>;
+    static bool done[64] = {};
+    cudaError_t e = configure(differential_core_kernel<T, D, R>, M::SMEM, done);
+    if (e != cudaSuccess) return e;
+    const int grid = p.W < sms ? p.W : sms;
+    differential_core_kernel<T, D, R><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+int differential_rows(int dtype, int D, int G) { return core_rows(dtype, D, G); }
+
+int differential_block_tokens(int dtype, int D, int G) {
+    const int most = core_rows(dtype, D, 128);
+    return G <= most ? most / G : 1;
+}
+
+int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes, int64_t max_len) {
+    int warps = 0;
+#define PKV_DF_WARPS(T, DD, RR) \
+    if (dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && D == DD && rows == RR) warps = CoreGeo<T, DD, RR>::WARPS;
+    PKV_DF_CORE(PKV_DF_WARPS)
+#undef PKV_DF_WARPS
+    const int64_t tiles = lanes * ((max_len + kTile - 1) / kTile);
+    int64_t w = (int64_t)warps * num_sms;
+    if (w > kMaxWorkers) w = kMaxWorkers / num_sms * num_sms;
+    if (tiles < w) w = tiles < 1 ? 1 : tiles;
+    return (int)w;
+}
+
+DifferentialLayout differential_layout(int D, int rows, int workers) {
+    DifferentialLayout L{};
+    L.rec = 0;
+    L.part_ml = up256(L.rec + sizeof(int4) * (size_t)workers);
+    L.part_o = up256(L.part_ml + sizeof(float2) * 2 * 2 * (size_t)workers * rows);
+    L.total = up256(L.part_o + sizeof(float) * 2 * 2 * 2 * (size_t)workers * rows * D);
+    return L;
+}
+
+cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) {
+    DfParams p{};
+    p.q = a.q;
+    p.q_bf16 = a.q_bf16;
+    p.k_new = a.k_new;
+    p.v_new = a.v_new;
+    p.k_pages = a.k_pages;
+    p.v_pages = a.v_pages;
+    p.n_pages = a.n_pages;
+    p.tables = a.tables;
+    p.max_pages = a.max_pages;
+    p.table_rows = a.table_rows;
+    p.seq_lens = a.seq_lens;
+    p.single_t = a.single_t;
+    p.max_seq_len = a.max_seq_len;
+    p.tok0 = a.tok0;
+    p.ntok = a.ntok;
+    p.B = a.B;
+    p.Hp = a.H / 2;
+    p.G = a.G;
+    p.R = a.rows;
+    p.subs = a.ntok ? (a.block_tokens * a.G + a.rows - 1) / a.rows : (a.G + a.rows - 1) / a.rows;
+    p.P = a.P;
+    p.window = a.window;
+    p.qscale = (float)(1.4426950408889634 / std::sqrt((double)a.D));
+    p.lambda = a.diff.lambda;
+    p.norm_weight = a.diff.norm_weight;
+    p.normalise = a.diff.normalise;
+    p.norm_eps = a.diff.norm_eps;
+    p.out_scale = a.diff.out_scale;
+    p.out = a.out;
+    p.W = a.workers;
+    p.err = a.dev_error;
+    const DifferentialLayout L = differential_layout(a.D, a.rows, a.workers);
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+    p.rec = reinterpret_cast<int4*>(ws + L.rec);
+    p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+    p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    if (a.ev_before) cudaEventRecord(a.ev_before, stream);
+    cudaError_t e = cudaErrorInvalidValue;
+#define PKV_DF_LAUNCH(T, DD, RR)                                                              \
+    if (a.dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && a.D == DD && a.rows == RR)        \
+        e = launch_core<T, DD, RR>(p, a.sms, stream);
+    PKV_DF_CORE(PKV_DF_LAUNCH)
+#undef PKV_DF_LAUNCH
+    if (e != cudaSuccess) return e;
+    if (a.ev_after) cudaEventRecord(a.ev_after, stream);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.W, (unsigned)p.R);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, differential_merge_kernel, p, a.D);
+}
+
+DifferentialChunkLayout differential_chunk_layout(int64_t N, int batch, int block_tokens, int D, int rows,
+                                                  int workers) {
+    DifferentialChunkLayout L{};
+    L.blocks = N / block_tokens + batch;
+    size_t at = differential_layout(D, rows, workers).total;
+    auto take = [&](int64_t n) {
+        const size_t o = at;
+        at = up256(at + sizeof(int32_t) * (size_t)n);
+        return o;
+    };
+    L.rows = take(L.blocks);
+    L.lens = take(L.blocks);
+    L.tok0 = take(L.blocks);
+    L.ntok = take(L.blocks);
+    L.first = take(batch + 1);
+    L.total = at;
+    return L;
+}
+
+cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, int64_t total_new,
+                                       const int32_t* cu_new, cudaStream_t stream) {
+    DifferentialArgs a = args;
+    const DifferentialChunkLayout L =
+        differential_chunk_layout(total_new, batch, a.block_tokens, a.D, a.rows, a.workers);
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+    ChunkParams c{};
+    c.B = batch;
+    c.H = a.H;
+    c.D = a.D;
+    c.P = a.P;
+    c.es = a.dtype == PKV_F32 ? 4 : 2;
+    c.bt = a.block_tokens;
+    c.N = total_new;
+    c.X = L.blocks;
+    c.n_pages = a.n_pages;
+    c.cu_new = cu_new;
+    c.seq_lens = a.seq_lens;
+    c.single_t = a.single_t;
+    c.tables = a.tables;
+    c.max_pages = a.max_pages;
+    c.k_new = a.k_new;
+    c.v_new = a.v_new;
+    c.k_pages = a.k_pages;
+    c.v_pages = a.v_pages;
+    c.rows = reinterpret_cast<int32_t*>(ws + L.rows);
+    c.lens = reinterpret_cast<int32_t*>(ws + L.lens);
+    c.tok0 = reinterpret_cast<int32_t*>(ws + L.tok0);
+    c.ntok = reinterpret_cast<int32_t*>(ws + L.ntok);
+    c.first = reinterpret_cast<int32_t*>(ws + L.first);
+    c.err = a.dev_error;
+    const int vec = a.D * c.es >= 16 ? 16 : 4;
+    const int64_t pieces = total_new * a.H * (a.D * c.es / vec);
+    const int64_t want = (pieces + 255) / 256, most = (int64_t)a.sms * 8;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    if (vec == 16) differential_append_kernel<16><<<grid, 256, 0, stream>>>(c);
+    else differential_append_kernel<4><<<grid, 256, 0, stream>>>(c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    differential_blocks_kernel<<<1, 1024, 0, stream>>>(c);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    a.k_new = a.v_new = nullptr;                    // stored already
+    a.B = (int)L.blocks;
+    a.table_rows = c.rows;
+    a.seq_lens = c.lens;
+    a.tok0 = c.tok0;
+    a.ntok = c.ntok;
+    a.max_seq_len = (int64_t)a.max_pages * a.P;
+    return launch_differential(a, stream);
+}
+
+}  // namespace pkv

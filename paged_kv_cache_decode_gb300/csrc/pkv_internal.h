@@ -7,7 +7,7 @@
 
 #include <cuda_runtime.h>
 
-struct pkv_pool;
+#include "pkv.h"
 
 namespace pkv {
 
@@ -260,5 +260,104 @@ cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, cudaStream_t stream)
 
 // DecodeArgs::before_split for a shared prefix: ctx is a SharedPrefixArgs.
 cudaError_t launch_shared_prefix_hook(const void* ctx, cudaStream_t stream);
+
+// ------------------------------------------------ differential attention --
+
+// One launch of the differential decode path for one layer.
+struct DifferentialArgs {
+    int dtype, B, H, G, D, P;   // H: KV heads (an even number); G: query pairs per KV pair
+    int64_t window;
+    const void* q;              // [B][2 * (H / 2) * G][D] fp32, or (q_bf16) bf16
+    bool q_bf16;
+    const void* k_new;          // [B][H][D] storage dtype; nullptr: no append
+    const void* v_new;
+    void* k_pages;              // this layer's pools, [pages][H][P][D]
+    void* v_pages;
+    int64_t n_pages;
+    const int32_t* tables;      // [B][max_pages], or rows chosen by table_rows
+    int max_pages;
+    const int32_t* table_rows;
+    const int32_t* seq_lens;    // [B] device; nullptr: single_t
+    int single_t;
+    int64_t max_seq_len;
+    const int32_t* tok0;        // prefill blocks (device): first chunk row and token count
+    const int32_t* ntok;
+    int block_tokens;           // most chunk tokens of a block (1: decode)
+    pkv_differential diff;
+    float* out;                 // [tokens][(H / 2) * G][2 D]
+    void* workspace;
+    int rows;                   // query rows of one lane (differential_rows)
+    int workers;                // differential_workers
+    int sms;
+    unsigned* dev_error;
+    cudaEvent_t ev_before;      // optional: recorded around the split kernel
+    cudaEvent_t ev_after;
+};
+
+// Byte offsets inside a differential workspace.
+struct DifferentialLayout {
+    size_t rec, part_ml, part_o, total;
+};
+
+// The same for a prefill through lanes: int32 arrays behind the decode workspace.
+struct DifferentialChunkLayout {
+    int64_t blocks;
+    size_t rows, lens, tok0, ntok, first, total;
+};
+
+// Query rows that share one pass over a lane's keys, for G query pairs per KV pair.
+int differential_rows(int dtype, int D, int G);
+
+// Chunk tokens of one lane of a prefill through lanes.
+int differential_block_tokens(int dtype, int D, int G);
+
+// Workers of one launch over `lanes` lanes of at most max_len attended positions.
+int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes, int64_t max_len);
+
+DifferentialLayout differential_layout(int D, int rows, int workers);
+DifferentialChunkLayout differential_chunk_layout(int64_t N, int batch, int block_tokens, int D, int rows,
+                                                  int workers);
+
+// Enqueue the split and merge kernels on `stream`.
+cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream);
+
+// Prefill through the same lanes: rows appended first, then blocks of chunk tokens.
+// a.seq_lens / a.single_t are the lengths after the chunk.
+cudaError_t launch_differential_chunks(const DifferentialArgs& a, int batch, int64_t total_new,
+                                       const int32_t* cu_new, cudaStream_t stream);
+
+// ------------------------------------------------------------------ pages --
+
+// A pool's storage: every layer's K and V pages, [layers][pages][H][P][row_bytes].
+struct PageStore {
+    void* k_base;
+    void* v_base;
+    int64_t layer_bytes, n_pages;
+    int layers, H, P, row_bytes, sms;
+    unsigned* dev_error;
+};
+
+constexpr int kInlinePairs = 480;    // (source, destination) pairs that travel with a launch
+
+// pages[dst[i]] = pages[src[i]] in every layer; device lists, or host lists.
+cudaError_t launch_copy_pages(const PageStore& s, int n, const int32_t* src, const int32_t* dst,
+                              cudaStream_t stream);
+cudaError_t launch_copy_page_list(const PageStore& s, int n, const int32_t* src, const int32_t* dst,
+                                  cudaStream_t stream);
+
+struct CompactArgs {
+    int batch;
+    int64_t total;                // kept rows of the whole batch
+    const int32_t* keep;          // [total] device
+    const int32_t* cu_keep;       // [batch + 1] device; nullptr: one request
+    const int32_t* tables;        // [batch][max_pages] device
+    int max_pages;
+    const int32_t* seq_lens;      // [batch] device; nullptr: single_t
+    int64_t single_t;
+    const int32_t* new_tables;    // [batch][new_max_pages] device
+    int new_max_pages;
+};
+
+cudaError_t launch_compact(const PageStore& s, const CompactArgs& a, cudaStream_t stream);
 
 }  // namespace pkv

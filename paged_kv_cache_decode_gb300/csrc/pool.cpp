@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -86,6 +87,7 @@ struct pkv_pool {
     cudaEvent_t ev_after = nullptr;
     bool tensor_cores = false;         // decode: K/V tiles by TMA tensor loads, products by MMA
     bool tmaps = false;                // tensor maps built (head_dim 64 or 128)
+    bool differential = false;         // requests carry the differential calls' scratch
     std::vector<CUtensorMap> tmap_k;   // per layer, when tmaps
     std::vector<CUtensorMap> tmap_v;
     // failure injection (pkv_pool_inject_fault), each hook one-shot
@@ -108,6 +110,8 @@ struct pkv_request {
     int appended_count = 0;
     pkv_counters counters{};
     int32_t* dev_table = nullptr;      // device copy, max_pages_per_request entries
+    int32_t* dev_table_other = nullptr;   // the same allocation's other half: a compaction reads
+                                       // one and leaves the new table in the other
     int64_t dev_dirty_from = 0;        // entries [dev_dirty_from, table.size()) not on the device
     void* dev_workspace = nullptr;
     size_t workspace_bytes = 0;
@@ -125,6 +129,8 @@ struct pkv_request {
     std::vector<uint8_t> cow_copied;
     void* dev_prefill_ws = nullptr;    // prefill scratch for one request's chunks
     size_t prefill_ws_bytes = 0;
+    void* dev_diff_ws = nullptr;       // scratch of the differential calls
+    size_t diff_ws_bytes = 0;
 };
 
 namespace {
@@ -245,6 +251,88 @@ bool encode_pool_map(CUtensorMap* map, void* base, int64_t rows, int D, int dtyp
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ---- differential calls --------------------------------------------------------
+
+int diff_rows(const pkv_pool* p) { return pkv::differential_rows(p->dtype, p->head_dim, p->group); }
+
+// Row blocks per (request, KV pair) of a decode.
+int64_t diff_subs(const pkv_pool* p) { return (p->group + diff_rows(p) - 1) / diff_rows(p); }
+
+int diff_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
+    return pkv::differential_workers(p->dtype, p->head_dim, diff_rows(p), p->sms,
+                                     requests * (p->heads / 2) * diff_subs(p),
+                                     pkv::attended_len(max_seq_len, p->window));
+}
+
+size_t diff_decode_bytes(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
+    return pkv::differential_layout(p->head_dim, diff_rows(p), diff_workers(p, requests, max_seq_len)).total;
+}
+
+// A prefill through lanes: blocks of bt chunk tokens are its requests.
+int diff_block_tokens(const pkv_pool* p) {
+    return pkv::differential_block_tokens(p->dtype, p->head_dim, p->group);
+}
+
+int diff_chunk_workers(const pkv_pool* p, int batch, int64_t n) {
+    return diff_workers(p, n / diff_block_tokens(p) + batch, p->max_context);
+}
+
+size_t diff_prefill_bytes(const pkv_pool* p, int batch, int64_t n) {
+    return pkv::differential_chunk_layout(n, batch, diff_block_tokens(p), p->head_dim, diff_rows(p),
+                                          diff_chunk_workers(p, batch, n)).total;
+}
+
+int check_diff(const pkv_pool* p, const pkv_differential* d, const void* out) {
+    if (!p->differential)
+        return fail(PKV_ERR_UNSUPPORTED, "the pool was not created with PKV_POOL_DIFFERENTIAL");
+    if (!d || !d->lambda) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL differential weights");
+    if (reinterpret_cast<uintptr_t>(d->lambda) % 4 || reinterpret_cast<uintptr_t>(d->norm_weight) % 4)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "lambda and norm_weight must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(out) % 16)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned");
+    if (!std::isfinite(d->out_scale)) return fail(PKV_ERR_INVALID_ARGUMENT, "out_scale is not finite");
+    if (d->normalise && !(d->norm_eps > 0.f && std::isfinite(d->norm_eps)))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "norm_eps must be positive and finite");
+    return PKV_OK;
+}
+
+// Everything of one layer's launch but inputs, lengths, tables and workspace.
+pkv::DifferentialArgs diff_args(pkv_pool* p, int layer, const pkv_differential* d) {
+    pkv::DifferentialArgs a{};
+    a.dtype = p->dtype;
+    a.H = p->heads;
+    a.G = p->group;
+    a.D = p->head_dim;
+    a.P = p->page_size;
+    a.window = p->window;
+    a.k_pages = static_cast<unsigned char*>(p->k_base) + (size_t)layer * p->layer_bytes;
+    a.v_pages = static_cast<unsigned char*>(p->v_base) + (size_t)layer * p->layer_bytes;
+    a.n_pages = p->pages;
+    a.block_tokens = 1;
+    a.diff = *d;
+    a.rows = diff_rows(p);
+    a.sms = p->sms;
+    a.dev_error = p->dev_error;
+    a.ev_before = p->ev_before;
+    a.ev_after = p->ev_after;
+    return a;
+}
+
+pkv::PageStore page_store(const pkv_pool* p) {
+    pkv::PageStore s{};
+    s.k_base = p->k_base;
+    s.v_base = p->v_base;
+    s.layer_bytes = (int64_t)p->layer_bytes;
+    s.n_pages = p->pages;
+    s.layers = p->layers;
+    s.H = p->heads;
+    s.P = p->page_size;
+    s.row_bytes = p->head_dim * elem_bytes(p->dtype);
+    s.sms = p->sms;
+    s.dev_error = p->dev_error;
+    return s;
+}
+
 void mark_dirty(pkv_request* r, int64_t from) {
     if (from < r->dev_dirty_from) r->dev_dirty_from = from;
 }
@@ -306,7 +394,7 @@ int check_device(const pkv_pool* p) {
 
 extern "C" {
 
-int pkv_version(void) { return 10000; }
+int pkv_version(void) { return 10100; }
 
 const char* pkv_last_error(void) { return g_last_error.c_str(); }
 
@@ -381,8 +469,10 @@ int pkv_pool_create_ex(const pkv_pool_options* opts, pkv_pool** out) {
                     layers, heads, head_dim, page_size, (long long)max_context, (long long)pages);
     if (dtype != PKV_F32 && dtype != PKV_BF16)
         return fail(PKV_ERR_INVALID_ARGUMENT, "dtype %d is neither PKV_F32 nor PKV_BF16", dtype);
-    if (flags & ~(PKV_POOL_HOST_ONLY | PKV_POOL_CUDA_CORES))
+    if (flags & ~(PKV_POOL_HOST_ONLY | PKV_POOL_CUDA_CORES | PKV_POOL_DIFFERENTIAL))
         return fail(PKV_ERR_INVALID_ARGUMENT, "unknown flags");
+    if ((flags & PKV_POOL_DIFFERENTIAL) && heads % 2 != 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "differential attention pairs heads: kv_heads %d is odd", heads);
     const bool host_only = (flags & PKV_POOL_HOST_ONLY) != 0;
     const int64_t per_request = (max_context + page_size - 1) / page_size;
     if (pages == 0) pages = per_request;
@@ -419,6 +509,7 @@ int pkv_pool_create_ex(const pkv_pool_options* opts, pkv_pool** out) {
     p->max_context = max_context;
     p->max_pages_per_request = per_request;
     p->host_only = host_only;
+    p->differential = (flags & PKV_POOL_DIFFERENTIAL) != 0;
 
     // free list: Fisher-Yates shuffle of 0..pages-1 with SplitMix64(seed)
     std::vector<int32_t> order((size_t)pages);
@@ -593,19 +684,25 @@ int pkv_request_create(pkv_pool* p, pkv_request** out) {
             pkv::workspace_layout(1, p->dec_heads, p->head_dim, r->workspace_workers, p->dec_group).total;
         if (p->tmaps && pkv::prefill_supported(p->dtype, p->head_dim, p->group))
             r->prefill_ws_bytes = pkv::prefill_workspace_bytes(1, p->group, p->max_context);
-        cudaError_t e = cudaMalloc(&r->dev_table, sizeof(int32_t) * (size_t)p->max_pages_per_request);
+        cudaError_t e = cudaMalloc(&r->dev_table, 2 * sizeof(int32_t) * (size_t)p->max_pages_per_request);
         if (e == cudaSuccess) e = cudaMalloc(&r->dev_workspace, r->workspace_bytes);
         if (e == cudaSuccess) e = cudaMemset(r->dev_workspace, 0, r->workspace_bytes);
         if (e == cudaSuccess && r->prefill_ws_bytes)
             e = cudaMalloc(&r->dev_prefill_ws, r->prefill_ws_bytes);
+        if (p->differential) {
+            r->diff_ws_bytes = diff_decode_bytes(p, 1, p->max_context);
+            if (e == cudaSuccess) e = cudaMalloc(&r->dev_diff_ws, r->diff_ws_bytes);
+        }
         if (e != cudaSuccess) {
             cudaFree(r->dev_table);
             cudaFree(r->dev_workspace);
             cudaFree(r->dev_prefill_ws);
+            cudaFree(r->dev_diff_ws);
             delete r;
             cudaGetLastError();
             return fail(PKV_ERR_OUT_OF_MEMORY, "cudaMalloc for request: %s", cudaGetErrorString(e));
         }
+        r->dev_table_other = r->dev_table + p->max_pages_per_request;
     }
     ++p->live_requests;
     *out = r;
@@ -618,9 +715,11 @@ int pkv_request_destroy(pkv_request* r) {
     if (r->pending) pkv_abort_token(r);
     for (int32_t pg : r->table) drop_page(p, pg, false);
     if (!p->host_only) {
-        cudaFree(r->dev_table);
+        // the two halves of one allocation trade places in a compaction
+        cudaFree(r->dev_table < r->dev_table_other ? r->dev_table : r->dev_table_other);
         cudaFree(r->dev_workspace);
         cudaFree(r->dev_prefill_ws);
+        cudaFree(r->dev_diff_ws);
     }
     --p->live_requests;
     delete r;
@@ -727,11 +826,8 @@ int begin_pending(pkv_request* r, int64_t n, bool chunk, int64_t* position) {
     return ok();
 }
 
-// Before a layer's first write for the pending positions: upload the changed
-// page-table entries and copy this layer's bytes of every shared page into its
-// private replacement.
-int prepare_layer_write(pkv_request* r, int layer, cudaStream_t s) {
-    pkv_pool* p = r->pool;
+// Bring the device's page table up to date.
+int upload_table(pkv_request* r, cudaStream_t s) {
     const int64_t n = (int64_t)r->table.size();
     if (r->dev_dirty_from < n) {
         cudaError_t e = cudaMemcpyAsync(r->dev_table + r->dev_dirty_from,
@@ -741,6 +837,15 @@ int prepare_layer_write(pkv_request* r, int layer, cudaStream_t s) {
         if (e != cudaSuccess) return cuda_fail(e, "page-table upload");
         r->dev_dirty_from = n;
     }
+    return PKV_OK;
+}
+
+// Before a layer's first write for the pending positions: upload the changed
+// page-table entries and copy this layer's bytes of every shared page into its
+// private replacement.
+int prepare_layer_write(pkv_request* r, int layer, cudaStream_t s) {
+    pkv_pool* p = r->pool;
+    if (int rc = upload_table(r, s); rc != PKV_OK) return rc;
     if (!r->cow.empty() && !r->cow_copied[(size_t)layer]) {
         const size_t page_bytes = (size_t)p->page_size * p->heads * p->head_dim * elem_bytes(p->dtype);
         char* kb = static_cast<char*>(p->k_base) + p->layer_bytes * (size_t)layer;
@@ -1206,6 +1311,15 @@ bool shared_kernel(const pkv_pool* p) {
     return p->tmaps && pkv::shared_prefix_supported(p->dtype, p->head_dim, p->group);
 }
 
+// A prefill of any differential pool, scratch checked by the caller.
+cudaError_t enqueue_diff_prefill(pkv_pool* p, pkv::DifferentialArgs& a, int batch, int64_t total_new,
+                                 const int32_t* cu_new, cudaStream_t s) {
+    a.q_bf16 = p->dtype == PKV_BF16;
+    a.block_tokens = diff_block_tokens(p);
+    a.workers = diff_chunk_workers(p, batch, total_new);
+    return pkv::launch_differential_chunks(a, batch, total_new, cu_new, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1281,6 +1395,368 @@ int pkv_paged_decode_attention_shared(pkv_pool* p, int layer, int batch, const f
     a.before_split_ctx = &sp;
     cudaError_t e = pkv::launch_decode(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "shared-prefix decode launch");
+    return ok();
+}
+
+int pkv_differential_workspace_size(const pkv_pool* p, int batch, int64_t max_seq_len, size_t* bytes) {
+    if (!p || !bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL argument");
+    if (batch < 0 || max_seq_len < 1) return fail(PKV_ERR_INVALID_ARGUMENT, "bad batch or length");
+    if (!p->differential)
+        return fail(PKV_ERR_UNSUPPORTED, "the pool was not created with PKV_POOL_DIFFERENTIAL");
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    *bytes = batch == 0 ? 0 : diff_decode_bytes(p, batch, max_seq_len);
+    return ok();
+}
+
+int pkv_paged_differential_decode(pkv_pool* p, int layer, int batch, const float* q, const void* k_new,
+                                  const void* v_new, const int32_t* page_tables, int max_pages,
+                                  const int32_t* seq_lens, int64_t max_seq_len,
+                                  const pkv_differential* diff, float* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    if (!p) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pool");
+    if (layer < 0 || layer >= p->layers)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "layer %d outside [0, %d)", layer, p->layers);
+    if (batch < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "negative batch");
+    if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
+    if (batch > 0) {
+        if (!q || !k_new || !v_new || !page_tables || !seq_lens || !out || !workspace)
+            return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
+        if (max_pages < 1 || max_seq_len < 1)
+            return fail(PKV_ERR_INVALID_ARGUMENT, "max_pages and max_seq_len must be >= 1");
+        if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+            return fail(PKV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+        if (int rc = check_rows_aligned(p, q, 4, k_new, v_new, out); rc != PKV_OK) return rc;
+    }
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (batch == 0) return ok();
+    const size_t need = diff_decode_bytes(p, batch, max_seq_len);
+    if (workspace_bytes < need)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    pkv::DifferentialArgs a = diff_args(p, layer, diff);
+    a.B = batch;
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.tables = page_tables;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.max_seq_len = max_seq_len;
+    a.out = out;
+    a.workspace = workspace;
+    a.workers = diff_workers(p, batch, max_seq_len);
+    cudaError_t e = pkv::launch_differential(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+    return ok();
+}
+
+int pkv_differential_prefill_workspace_size(const pkv_pool* p, int batch, int64_t total_new,
+                                            size_t* bytes) {
+    if (!p || !bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL argument");
+    if (batch < 0 || total_new < 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "negative batch or token count");
+    if (!p->differential)
+        return fail(PKV_ERR_UNSUPPORTED, "the pool was not created with PKV_POOL_DIFFERENTIAL");
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    *bytes = (batch == 0 || total_new == 0) ? 0 : diff_prefill_bytes(p, batch, total_new);
+    return ok();
+}
+
+int pkv_paged_differential_prefill(pkv_pool* p, int layer, int batch, int64_t total_new, const void* q,
+                                   const void* k_new, const void* v_new, const int32_t* cu_new,
+                                   const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
+                                   const pkv_differential* diff, float* out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    if (!p) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pool");
+    if (layer < 0 || layer >= p->layers)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "layer %d outside [0, %d)", layer, p->layers);
+    if (batch < 0 || total_new < 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "negative batch or token count");
+    if (total_new + batch > INT32_MAX) return fail(PKV_ERR_INVALID_ARGUMENT, "more than 2^31 - 1 tokens");
+    if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (batch == 0 || total_new == 0) return ok();
+    if (!q || !k_new || !v_new || !cu_new || !page_tables || !seq_lens || !out || !workspace)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
+    if (max_pages < 1) return fail(PKV_ERR_INVALID_ARGUMENT, "max_pages must be >= 1");
+    if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+    if (int rc = check_rows_aligned(p, q, elem_bytes(p->dtype), k_new, v_new, out); rc != PKV_OK)
+        return rc;
+    const size_t need = diff_prefill_bytes(p, batch, total_new);
+    if (workspace_bytes < need)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    pkv::DifferentialArgs a = diff_args(p, layer, diff);
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.tables = page_tables;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.workspace = workspace;
+    cudaError_t e = enqueue_diff_prefill(p, a, batch, total_new, cu_new, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+    return ok();
+}
+
+int pkv_append_and_attend_differential(pkv_request* r, int layer, const float* q, const void* k,
+                                       const void* v, const pkv_differential* diff, float* out,
+                                       void* stream) {
+    if (!r) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL request");
+    pkv_pool* p = r->pool;
+    if (!q || !k || !v || !out) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if (layer < 0 || layer >= p->layers)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "layer %d outside [0, %d)", layer, p->layers);
+    if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
+    if (int rc = check_rows_aligned(p, q, 4, k, v, out); rc != PKV_OK) return rc;
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (!r->pending) return fail(PKV_ERR_BAD_STATE, "no token pending");
+    if (r->chunk)
+        return fail(PKV_ERR_BAD_STATE, "a chunk is pending (pkv_prefill_chunk_differential)");
+    if (r->appended[(size_t)layer]) return fail(PKV_ERR_BAD_STATE, "layer %d already ran", layer);
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    if (layer_fault(p, layer)) return fail(PKV_ERR_CUDA, "injected failure on layer %d", layer);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = prepare_layer_write(r, layer, s); rc != PKV_OK) return rc;
+    pkv::DifferentialArgs a = diff_args(p, layer, diff);
+    a.B = 1;
+    a.q = q;
+    a.k_new = k;
+    a.v_new = v;
+    a.tables = r->dev_table;
+    a.max_pages = (int)p->max_pages_per_request;
+    a.single_t = (int)(r->position + 1);
+    a.max_seq_len = r->position + 1;
+    a.out = out;
+    a.workspace = r->dev_diff_ws;
+    a.workers = diff_workers(p, 1, r->position + 1);
+    cudaError_t e = pkv::launch_differential(a, s);
+    if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+    r->appended[(size_t)layer] = 1;
+    ++r->appended_count;
+    return ok();
+}
+
+int pkv_prefill_chunk_differential(pkv_request* r, int layer, const void* q, const void* k, const void* v,
+                                   const pkv_differential* diff, float* out, void* stream) {
+    if (!r) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL request");
+    pkv_pool* p = r->pool;
+    if (!q || !k || !v || !out) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if (layer < 0 || layer >= p->layers)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "layer %d outside [0, %d)", layer, p->layers);
+    if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
+    if (int rc = check_rows_aligned(p, q, elem_bytes(p->dtype), k, v, out); rc != PKV_OK) return rc;
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (!r->pending || !r->chunk) return fail(PKV_ERR_BAD_STATE, "no chunk pending");
+    if (r->appended[(size_t)layer]) return fail(PKV_ERR_BAD_STATE, "layer %d already ran", layer);
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    if (layer_fault(p, layer)) return fail(PKV_ERR_CUDA, "injected failure on layer %d", layer);
+    const size_t need = diff_prefill_bytes(p, 1, r->pending_n);
+    if (r->diff_ws_bytes < need) {
+        void* ws = nullptr;
+        if (cudaMalloc(&ws, need) != cudaSuccess) {
+            cudaGetLastError();
+            return fail(PKV_ERR_OUT_OF_MEMORY, "prefill scratch of %zu bytes", need);
+        }
+        cudaFree(r->dev_diff_ws);
+        r->dev_diff_ws = ws;
+        r->diff_ws_bytes = need;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int rc = prepare_layer_write(r, layer, s); rc != PKV_OK) return rc;
+    pkv::DifferentialArgs a = diff_args(p, layer, diff);
+    a.q = q;
+    a.k_new = k;
+    a.v_new = v;
+    a.tables = r->dev_table;
+    a.max_pages = (int)p->max_pages_per_request;
+    a.single_t = (int)(r->position + r->pending_n);
+    a.out = out;
+    a.workspace = r->dev_diff_ws;
+    cudaError_t e = enqueue_diff_prefill(p, a, 1, r->pending_n, nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+    r->appended[(size_t)layer] = 1;
+    ++r->appended_count;
+    return ok();
+}
+
+int pkv_copy_pages(pkv_pool* p, int n, const int32_t* src_pages, const int32_t* dst_pages, void* stream) {
+    if (!p) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pool");
+    if (n < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "negative page count %d", n);
+    if (n > 0 && (!src_pages || !dst_pages)) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (n == 0) return ok();
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    cudaError_t e =
+        pkv::launch_copy_pages(page_store(p), n, src_pages, dst_pages, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+    return ok();
+}
+
+int pkv_compact_pages(pkv_pool* p, int batch, int64_t total_keep, const int32_t* keep,
+                      const int32_t* cu_keep, const int32_t* page_tables, int max_pages,
+                      const int32_t* seq_lens, const int32_t* new_tables, int new_max_pages,
+                      void* stream) {
+    if (!p) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pool");
+    if (batch < 0 || total_keep < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "negative batch or row count");
+    if (total_keep > INT32_MAX) return fail(PKV_ERR_INVALID_ARGUMENT, "more than 2^31 - 1 rows");
+    if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
+    if (batch == 0 || total_keep == 0) return ok();
+    if (!keep || !cu_keep || !page_tables || !seq_lens || !new_tables)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
+    if (max_pages < 1 || new_max_pages < 1)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "max_pages and new_max_pages must be >= 1");
+    if (int rc = check_device(p); rc != PKV_OK) return rc;
+    pkv::CompactArgs a{};
+    a.batch = batch;
+    a.total = total_keep;
+    a.keep = keep;
+    a.cu_keep = cu_keep;
+    a.tables = page_tables;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.new_tables = new_tables;
+    a.new_max_pages = new_max_pages;
+    cudaError_t e = pkv::launch_compact(page_store(p), a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
+    return ok();
+}
+
+int pkv_request_fork_batch(const pkv_request* parent, int n, pkv_request** children, void* stream) {
+    if (!parent || n < 0 || (n > 0 && !children)) return fail(PKV_ERR_INVALID_ARGUMENT, "bad argument");
+    for (int i = 0; i < n; ++i) children[i] = nullptr;
+    if (parent->pending) return fail(PKV_ERR_BAD_STATE, "the parent has a token pending");
+    pkv_pool* p = parent->pool;
+    const int64_t full = parent->length / p->page_size;
+    const bool tail = parent->length % p->page_size != 0;
+    if (tail && n > (int64_t)p->free_list.size())
+        return fail(PKV_ERR_OUT_OF_PAGES, "%d pages needed, %lld free", n, (long long)p->free_list.size());
+    if (n == 0) return ok();
+    if (!p->host_only)
+        if (int rc = check_device(p); rc != PKV_OK) return rc;
+    if (lease_fault(p, tail ? n : 0)) return fail(PKV_ERR_OUT_OF_PAGES, "injected lease failure");
+    int rc = PKV_OK, made = 0;
+    std::vector<int32_t> src, dst;
+    try {
+        src.reserve((size_t)n);
+        dst.reserve((size_t)n);
+        for (; made < n; ++made)
+            if ((rc = pkv_request_create(p, &children[made])) != PKV_OK) break;
+    } catch (const std::bad_alloc&) {
+        rc = fail(PKV_ERR_OUT_OF_MEMORY, "host allocation failed");
+    }
+    if (rc == PKV_OK) {
+        // every table was reserved for a whole context: nothing below allocates
+        for (int i = 0; i < n; ++i) {
+            pkv_request* c = children[i];
+            c->table.assign(parent->table.begin(), parent->table.begin() + full);
+            for (int32_t pg : c->table) ++p->refs[(size_t)pg];
+            if (tail) {
+                const int32_t page = lease_front(p);
+                c->table.push_back(page);
+                src.push_back(parent->table[(size_t)full]);
+                dst.push_back(page);
+            }
+            c->length = parent->length;
+            c->dev_dirty_from = 0;
+        }
+        if (tail && !p->host_only) {
+            cudaError_t e = pkv::launch_copy_page_list(page_store(p), n, src.data(), dst.data(),
+                                                       static_cast<cudaStream_t>(stream));
+            if (e != cudaSuccess) rc = cuda_fail(e, "page copy launch");
+        }
+    }
+    if (rc != PKV_OK) {
+        const std::string why = g_last_error;
+        for (int i = made - 1; i >= 0; --i) {
+            pkv_request* c = children[i];
+            if (tail && !c->table.empty()) {        // leased last, back to the front first
+                drop_page(p, c->table.back(), true);
+                c->table.pop_back();
+            }
+            pkv_request_destroy(c);
+        }
+        for (int i = 0; i < n; ++i) children[i] = nullptr;
+        g_last_error = why;
+        return rc;
+    }
+    return ok();
+}
+
+int pkv_request_truncate(pkv_request* r, int64_t length) {
+    if (!r) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL request");
+    if (r->pending) return fail(PKV_ERR_BAD_STATE, "a token is pending");
+    if (length < 0 || length > r->length)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "length %lld outside [0, %lld]", (long long)length,
+                    (long long)r->length);
+    const size_t keep = (size_t)((length + r->pool->page_size - 1) / r->pool->page_size);
+    for (size_t i = keep; i < r->table.size(); ++i) drop_page(r->pool, r->table[i], false);
+    if (keep < r->table.size()) {
+        r->table.resize(keep);
+        mark_dirty(r, (int64_t)keep);
+    }
+    r->length = length;
+    return ok();
+}
+
+int pkv_request_compact(pkv_request* r, int64_t n, const int32_t* keep, void* stream) {
+    if (!r) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL request");
+    pkv_pool* p = r->pool;
+    if (r->pending) return fail(PKV_ERR_BAD_STATE, "a token is pending");
+    if (n < 0 || n > r->length)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "%lld positions kept of %lld", (long long)n,
+                    (long long)r->length);
+    if (n > 0 && !keep && !p->host_only) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
+    if (n > INT32_MAX) return fail(PKV_ERR_INVALID_ARGUMENT, "more than 2^31 - 1 rows");
+    const int64_t pages = (n + p->page_size - 1) / p->page_size;
+    if (pages > (int64_t)p->free_list.size())
+        return fail(PKV_ERR_OUT_OF_PAGES, "%lld pages needed, %lld free", (long long)pages,
+                    (long long)p->free_list.size());
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!p->host_only)
+        if (int rc = check_device(p); rc != PKV_OK) return rc;
+    std::vector<int32_t> old;
+    try {
+        old.reserve((size_t)p->max_pages_per_request);   // becomes the new table's storage
+    } catch (const std::bad_alloc&) {
+        return fail(PKV_ERR_OUT_OF_MEMORY, "host allocation failed");
+    }
+    if (lease_fault(p, pages)) return fail(PKV_ERR_OUT_OF_PAGES, "injected lease failure");
+    if (!p->host_only && n > 0)
+        if (int rc = upload_table(r, s); rc != PKV_OK) return rc;
+    const int64_t length = r->length;
+    old.swap(r->table);
+    for (int64_t i = 0; i < pages; ++i) r->table.push_back(lease_front(p));
+    if (!p->host_only && n > 0) {
+        cudaError_t e = cudaMemcpyAsync(r->dev_table_other, r->table.data(),
+                                        sizeof(int32_t) * (size_t)pages, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) {
+            pkv::CompactArgs a{};
+            a.batch = 1;
+            a.total = n;
+            a.keep = keep;
+            a.tables = r->dev_table;
+            a.max_pages = (int)old.size();
+            a.single_t = length;
+            a.new_tables = r->dev_table_other;
+            a.new_max_pages = (int)pages;
+            e = pkv::launch_compact(page_store(p), a, s);
+        }
+        if (e != cudaSuccess) {
+            while (!r->table.empty()) {             // leased last, back to the front first
+                drop_page(p, r->table.back(), true);
+                r->table.pop_back();
+            }
+            old.swap(r->table);
+            return cuda_fail(e, "compaction launch");
+        }
+        std::swap(r->dev_table, r->dev_table_other);
+    }
+    for (int32_t pg : old) drop_page(p, pg, false);
+    r->dev_dirty_from = pages;
+    r->length = n;
     return ok();
 }
 
