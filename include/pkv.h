@@ -618,8 +618,10 @@ int pkv_paged_differential_decode(pkv_pool* pool, int layer, int batch, const fl
                                   const pkv_differential* diff, float* out, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
-/* Device scratch bytes that pkv_paged_differential_prefill needs (0 when batch or
- * total_new is 0). */
+/* Device scratch bytes that pkv_paged_differential_prefill needs: 0 when batch or
+ * total_new is 0, and for pools whose prefill runs on the tensor cores (bf16,
+ * head_dim 64 or 128); else the scratch of a decode of total_new requests, or of
+ * blocks of their tokens. */
 int pkv_differential_prefill_workspace_size(const pkv_pool* pool, int batch, int64_t total_new,
                                             size_t* bytes);
 
@@ -628,8 +630,12 @@ int pkv_differential_prefill_workspace_size(const pkv_pool* pool, int batch, int
  * and causal rule (chunk token i of request b attends positions 0 .. L0_b + i, the
  * last `window` of them), with
  *   out          [total_new][query_heads / 2][2 head_dim] fp32, device, 16-byte aligned
- *   workspace    >= pkv_differential_prefill_workspace_size bytes, 16-byte aligned
- * A request with n_b = 0 appends nothing.  Bad lengths or page ids set the pool's
+ *   workspace    >= pkv_differential_prefill_workspace_size bytes, 16-byte aligned;
+ *                may be NULL when that is 0
+ * bf16 pools of head_dim 64 or 128 run on the tcgen05 tensor cores (bf16 products
+ * with fp32 accumulation, the weights as bf16 hi + lo; two kernels: append,
+ * attention).  Every other pool runs chunk tokens, or blocks of them, as lanes of
+ * the decode kernel (four kernels: append, blocks, split, merge).  A request with n_b = 0 appends nothing.  Bad lengths or page ids set the pool's
  * error word; the affected rows are then unspecified, rows at or past
  * cu_new[batch] are left as they were.
  */

@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 
-SOURCES = ["decode.cu", "differential.cu", "prefill.cu", "shared_prefix.cu", "pages.cu", "pool.cpp",
-           "static_scratch.cu"]
+SOURCES = ["decode.cu", "differential.cu", "differential_prefill.cu", "prefill.cu", "shared_prefix.cu",
+           "pages.cu", "pool.cpp", "static_scratch.cu"]
 HEADERS = [os.path.join(CSRC, "pkv_internal.h"), os.path.join(CSRC, "ptx.cuh"),
            os.path.join(CSRC, "tc05.cuh"),
            os.path.join(INCLUDE, "pkv.h")]

@@ -731,6 +731,7 @@ __device__ __forceinline__ bool chunk_ok(const ChunkParams& p, int b) {
 // Every new key / value row into its page: VEC bytes a thread.
 template <int VEC>
 __global__ void __launch_bounds__(256) differential_append_kernel(const ChunkParams p) {
+    pdl_launch_dependents();                    // an attention grid may start; it waits for the rows
     const int pieces = p.D * p.es / VEC;
     const int64_t total = p.N * p.H * pieces;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
@@ -978,12 +979,9 @@ DifferentialChunkLayout differential_chunk_layout(int64_t N, int batch, int bloc
     return L;
 }
 
-cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, int64_t total_new,
-                                       const int32_t* cu_new, cudaStream_t stream) {
-    DifferentialArgs a = args;
-    const DifferentialChunkLayout L =
-        differential_chunk_layout(total_new, batch, a.block_tokens, a.D, a.rows, a.workers);
-    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+namespace {
+
+ChunkParams chunk_params(const DifferentialArgs& a, int batch, int64_t total_new, const int32_t* cu_new) {
     ChunkParams c{};
     c.B = batch;
     c.H = a.H;
@@ -992,7 +990,6 @@ cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, 
     c.es = a.dtype == PKV_F32 ? 4 : 2;
     c.bt = a.block_tokens;
     c.N = total_new;
-    c.X = L.blocks;
     c.n_pages = a.n_pages;
     c.cu_new = cu_new;
     c.seq_lens = a.seq_lens;
@@ -1003,19 +1000,38 @@ cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, 
     c.v_new = a.v_new;
     c.k_pages = a.k_pages;
     c.v_pages = a.v_pages;
-    c.rows = reinterpret_cast<int32_t*>(ws + L.rows);
-    c.lens = reinterpret_cast<int32_t*>(ws + L.lens);
-    c.tok0 = reinterpret_cast<int32_t*>(ws + L.tok0);
-    c.ntok = reinterpret_cast<int32_t*>(ws + L.ntok);
-    c.first = reinterpret_cast<int32_t*>(ws + L.first);
     c.err = a.dev_error;
+    return c;
+}
+
+}  // namespace
+
+cudaError_t launch_differential_append(const DifferentialArgs& a, int batch, int64_t total_new,
+                                       const int32_t* cu_new, cudaStream_t stream) {
+    const ChunkParams c = chunk_params(a, batch, total_new, cu_new);
     const int vec = a.D * c.es >= 16 ? 16 : 4;
     const int64_t pieces = total_new * a.H * (a.D * c.es / vec);
     const int64_t want = (pieces + 255) / 256, most = (int64_t)a.sms * 8;
     const unsigned grid = (unsigned)(want < most ? want : most);
     if (vec == 16) differential_append_kernel<16><<<grid, 256, 0, stream>>>(c);
     else differential_append_kernel<4><<<grid, 256, 0, stream>>>(c);
-    cudaError_t e = cudaGetLastError();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, int64_t total_new,
+                                       const int32_t* cu_new, cudaStream_t stream) {
+    DifferentialArgs a = args;
+    const DifferentialChunkLayout L =
+        differential_chunk_layout(total_new, batch, a.block_tokens, a.D, a.rows, a.workers);
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+    ChunkParams c = chunk_params(a, batch, total_new, cu_new);
+    c.X = L.blocks;
+    c.rows = reinterpret_cast<int32_t*>(ws + L.rows);
+    c.lens = reinterpret_cast<int32_t*>(ws + L.lens);
+    c.tok0 = reinterpret_cast<int32_t*>(ws + L.tok0);
+    c.ntok = reinterpret_cast<int32_t*>(ws + L.ntok);
+    c.first = reinterpret_cast<int32_t*>(ws + L.first);
+    cudaError_t e = launch_differential_append(a, batch, total_new, cu_new, stream);
     if (e != cudaSuccess) return e;
     differential_blocks_kernel<<<1, 1024, 0, stream>>>(c);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -326,6 +326,21 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream);
 cudaError_t launch_differential_chunks(const DifferentialArgs& a, int batch, int64_t total_new,
                                        const int32_t* cu_new, cudaStream_t stream);
 
+// Store a chunk's k_new / v_new rows in their pages.
+cudaError_t launch_differential_append(const DifferentialArgs& a, int batch, int64_t total_new,
+                                       const int32_t* cu_new, cudaStream_t stream);
+
+// Prefill on the tensor cores (bf16, head width 64 or 128): no scratch.  tmap_k, tmap_v:
+// the layer's CUtensorMaps (host memory).
+bool differential_prefill_supported(int dtype, int D, int G);
+
+// Upper bound on the query tiles of a call.
+int64_t differential_prefill_tiles(int B, int G, int64_t total_new);
+
+cudaError_t launch_differential_prefill(const DifferentialArgs& a, int batch, int64_t total_new,
+                                        const int32_t* cu_new, const void* tmap_k, const void* tmap_v,
+                                        cudaStream_t stream);
+
 // ------------------------------------------------------------------ pages --
 
 // A pool's storage: every layer's K and V pages, [layers][pages][H][P][row_bytes].

@@ -277,7 +277,13 @@ int diff_chunk_workers(const pkv_pool* p, int batch, int64_t n) {
     return diff_workers(p, n / diff_block_tokens(p) + batch, p->max_context);
 }
 
+// The tensor-core prefill serves the pool (it needs no scratch); else lanes.
+bool diff_tensor_prefill(const pkv_pool* p) {
+    return p->tmaps && pkv::differential_prefill_supported(p->dtype, p->head_dim, p->group);
+}
+
 size_t diff_prefill_bytes(const pkv_pool* p, int batch, int64_t n) {
+    if (diff_tensor_prefill(p)) return 0;
     return pkv::differential_chunk_layout(n, batch, diff_block_tokens(p), p->head_dim, diff_rows(p),
                                           diff_chunk_workers(p, batch, n)).total;
 }
@@ -1312,8 +1318,11 @@ bool shared_kernel(const pkv_pool* p) {
 }
 
 // A prefill of any differential pool, scratch checked by the caller.
-cudaError_t enqueue_diff_prefill(pkv_pool* p, pkv::DifferentialArgs& a, int batch, int64_t total_new,
-                                 const int32_t* cu_new, cudaStream_t s) {
+cudaError_t enqueue_diff_prefill(pkv_pool* p, int layer, pkv::DifferentialArgs& a, int batch,
+                                 int64_t total_new, const int32_t* cu_new, cudaStream_t s) {
+    if (diff_tensor_prefill(p))
+        return pkv::launch_differential_prefill(a, batch, total_new, cu_new, &p->tmap_k[(size_t)layer],
+                                                &p->tmap_v[(size_t)layer], s);
     a.q_bf16 = p->dtype == PKV_BF16;
     a.block_tokens = diff_block_tokens(p);
     a.workers = diff_chunk_workers(p, batch, total_new);
@@ -1476,14 +1485,18 @@ int pkv_paged_differential_prefill(pkv_pool* p, int layer, int batch, int64_t to
     if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
     if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
     if (batch == 0 || total_new == 0) return ok();
-    if (!q || !k_new || !v_new || !cu_new || !page_tables || !seq_lens || !out || !workspace)
+    const size_t need = diff_prefill_bytes(p, batch, total_new);
+    if (!q || !k_new || !v_new || !cu_new || !page_tables || !seq_lens || !out || (need && !workspace))
         return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
     if (max_pages < 1) return fail(PKV_ERR_INVALID_ARGUMENT, "max_pages must be >= 1");
     if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
         return fail(PKV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
     if (int rc = check_rows_aligned(p, q, elem_bytes(p->dtype), k_new, v_new, out); rc != PKV_OK)
         return rc;
-    const size_t need = diff_prefill_bytes(p, batch, total_new);
+    if (diff_tensor_prefill(p) &&
+        pkv::differential_prefill_tiles(batch, p->group, total_new) * p->heads > INT32_MAX)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "%lld tokens need more CTAs than one launch holds",
+                    (long long)total_new);
     if (workspace_bytes < need)
         return fail(PKV_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if (int rc = check_device(p); rc != PKV_OK) return rc;
@@ -1496,7 +1509,7 @@ int pkv_paged_differential_prefill(pkv_pool* p, int layer, int batch, int64_t to
     a.seq_lens = seq_lens;
     a.out = out;
     a.workspace = workspace;
-    cudaError_t e = enqueue_diff_prefill(p, a, batch, total_new, cu_new, static_cast<cudaStream_t>(stream));
+    cudaError_t e = enqueue_diff_prefill(p, layer, a, batch, total_new, cu_new, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
     return ok();
 }
@@ -1575,7 +1588,7 @@ int pkv_prefill_chunk_differential(pkv_request* r, int layer, const void* q, con
     a.single_t = (int)(r->position + r->pending_n);
     a.out = out;
     a.workspace = r->dev_diff_ws;
-    cudaError_t e = enqueue_diff_prefill(p, a, 1, r->pending_n, nullptr, s);
+    cudaError_t e = enqueue_diff_prefill(p, layer, a, 1, r->pending_n, nullptr, s);
     if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
     r->appended[(size_t)layer] = 1;
     ++r->appended_count;
