@@ -202,6 +202,66 @@ __device__ __forceinline__ void cursor_next(const DfParams& p, Cursor& c) {
     if (c.x < p.B) cursor_load(p, c);
 }
 
+// Page ids of a cursor's tiles, 32 table entries at a time: lane i holds entry base + i.
+struct Pager {
+    int x = -1, base = 0;
+    int32_t val = -1;
+
+    __device__ __forceinline__ int32_t page(const DfParams& p, const Cursor& c, int index) {
+        if (c.x != x || index < base || index >= base + 32) {
+            x = c.x;
+            base = index;
+            const int e = index + (int)(threadIdx.x & 31);
+            const int64_t row = p.table_rows ? __ldg(p.table_rows + x) : x;
+            val = e < p.max_pages ? __ldg(p.tables + row * p.max_pages + e) : -1;
+        }
+        return __shfl_sync(0xffffffffu, val, index - base);
+    }
+};
+
+// One worker's share of the flattened tiles (every worker that works has one at least).
+struct Share {
+    int64_t all, begin;         // tiles of the launch, first of this worker
+    int workers, n;             // workers with work, tiles of this one (0: none)
+};
+
+__device__ __forceinline__ Share share_of(const DfParams& p, int64_t requests_tiles, int w) {
+    Share s;
+    s.all = (int64_t)p.Hp * p.subs * requests_tiles;
+    s.workers = (int)(s.all < p.W ? s.all : p.W);
+    s.n = 0;
+    s.begin = 0;
+    if (w >= s.workers) return s;
+    s.begin = w * s.all / s.workers;
+    s.n = (int)((w + 1) * s.all / s.workers - s.begin);
+    return s;
+}
+
+// The last worker of a lane that ends before flattened tile `lane_end`: the inverse of
+// `begin` above.
+__device__ __forceinline__ int last_worker(const Share& s, int64_t lane_end) {
+    return (int)((lane_end * s.workers - 1) / s.all);
+}
+
+// Empty slots of the batch: their rows of the output are zeros.  All threads of all CTAs.
+__device__ __forceinline__ void zero_empty(const DfParams& p, int D) {
+    if (p.tok0) return;
+    const int n = p.Hp * p.G * 2 * D;
+    for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
+        if (tiles_at(p, x) > 0) continue;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) p.out[(int64_t)x * n + i] = 0.f;
+    }
+}
+
+// A wait ran out: report it and let the copies in flight behind stage s land.
+__device__ __forceinline__ void give_up(const DfParams& p, uint64_t* bars, int stages, int s, uint32_t parity,
+                                        int ahead) {
+    if ((threadIdx.x & 31) != 0) return;
+    atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+    for (int i = 1; i < stages && i < ahead; ++i)
+        mbar_wait_bounded(&bars[(s + i) % stages], parity ^ (s + i >= stages ? 1u : 0u), kWaitNs);
+}
+
 // The rows of one lane: row r is query pair `head` of one token, at output row `row`
 // ([token][Hp * G]), attending positions start .. end - 1.
 struct LaneRows {
@@ -312,40 +372,21 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
     }
     int stride, entries;
     const int64_t total = build_prefix(p, prefix, stride, entries);
-    const int LN = p.Hp * p.subs;
-
-    // empty slots: their rows of the output are zeros
-    for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
-        if (p.tok0 || tiles_at(p, x) > 0) continue;
-        float* o = p.out + (int64_t)x * p.Hp * p.G * 2 * D;
-        for (int i = threadIdx.x; i < p.Hp * p.G * 2 * D; i += blockDim.x) o[i] = 0.f;
-    }
-
-    const int64_t T_all = LN * total;
-    const int64_t We = T_all < p.W ? T_all : p.W;   // every worker that works has a tile
-    if (w >= We) return;
-    const int64_t begin = w * T_all / We, end = (w + 1) * T_all / We;
-    const int n_work = (int)(end - begin);
-    Cursor cur = cursor_at(p, prefix, stride, entries, begin);
+    zero_empty(p, D);
+    const Share share = share_of(p, total, w);
+    if (share.n == 0) return;
+    const int n_work = share.n;
+    Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
     Cursor prod = cur;
-    int64_t f = begin;                              // flattened index of cur
+    Pager pager;
+    int64_t f = share.begin;                        // flattened index of cur
     const uint64_t policy = l2_stream_policy();
     const int tpp = p.P / kTile;
 
-    // lane i holds table entry tab_base + i of request tab_x
-    int tab_x = -1, tab_base = 0;
-    int32_t tab_val = -1;
     auto issue = [&](int s) {
         const int gt = prod.tile0 + prod.tile;
         const int pi = gt / tpp;
-        if (prod.x != tab_x || pi < tab_base || pi >= tab_base + 32) {
-            tab_x = prod.x;
-            tab_base = pi;
-            const int e = pi + lane;
-            const int64_t row = p.table_rows ? __ldg(p.table_rows + tab_x) : tab_x;
-            tab_val = e < p.max_pages ? __ldg(p.tables + row * p.max_pages + e) : -1;
-        }
-        const int32_t page = __shfl_sync(0xffffffffu, tab_val, pi - tab_base);
+        const int32_t page = pager.page(p, prod, pi);
         if (lane == 0) {
             stage_page[s] = page;
             if (page < 0 || page >= p.n_pages) {
@@ -407,14 +448,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
             }
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            if (lane == 0) {
-                atomicOr(p.err, PKV_DEVERR_TIMEOUT);
-                // copies of the other stages may still be in flight
-                for (int i = 1; i < M::STAGES && k + i < issued; ++i) {
-                    const int si = (s + i) % M::STAGES;
-                    mbar_wait_bounded(&bars[si], parity ^ (s + i >= M::STAGES ? 1u : 0u), kWaitNs);
-                }
-            }
+            give_up(p, bars, M::STAGES, s, parity, issued - k);
             return;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
@@ -594,8 +628,475 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
                 }
             }
             if (has_start && !has_end && lane == 0) {
-                const int64_t lane_end = f - cur.tile + cur.n;
-                p.rec[w] = make_int4(cur.x, cur.ln, (int)((lane_end * We - 1) / T_all), 1);
+                p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, f - cur.tile + cur.n), 1);
+            }
+        }
+        cursor_next(p, cur);
+    }
+}
+
+// ------------------------------------------------------ tensor-core engine --
+
+// bf16, head width 64 or 128, R = 1, 2, 4 or 8 query rows a lane.  A stage holds a tile as
+// TMA leaves it, K then V: [head][64-column chunk][16 rows][128 bytes], 128-byte swizzle
+// (one box of a 5-D map for both heads).  Products are m16n8k16 with the cache as the
+// 16-row operand, so that few queries still fill the 8 columns:
+//   S_m = K_m Q_m^T   16 keys x 8 columns of queries.  fp32 queries go in as bf16 parts
+//                     (hi, mid, lo: 24 bits) on columns of their own where there is
+//                     room, else as further products into the same columns
+//   O += V^T P^T      16 value columns x 8 columns of (query, map, part of the weight);
+//                     P^T is the scores' fragment transposed by movmatrix, weights as
+//                     three bf16 parts too.  Both maps share every V fragment
+// Column layouts (lane = 4 g + t holds columns 2t, 2t + 1 of row g and row g + 8):
+//   R   S columns 2t, 2t+1              O columns 2t, 2t+1               MMAs a tile (D 128)
+//   1   t even: hi, mid; odd: lo, 0     map t/2; t even: hi, mid; odd: lo, 0    16 + 16
+//   2   query t/2, as above             query t/2, map t%2: hi, mid; + lo, 0    16 + 32
+//   4   query t: hi, mid; + lo, 0       query t: map 0, map 1; parts added      32 + 48
+//   8   queries 2t, 2t+1; parts added   the same, an accumulator a map          32 + 96
+// (R = 8 at D = 128 takes two parts of q, 2^-18: three do not fit the registers.)
+// mma.sync, not tcgen05: at most 16 columns of queries would use 16 of tcgen05's 128
+// rows, and the kernel waits for memory.  Each tile's V product is added to O by
+// rounding adds: the MMA's own accumulation truncates, which over a long cache adds up
+// (1.3e-5 of the result at 131072 keys).  The maximum is only followed when it grows by
+// more than 8 in log2 units: weights stay below 2^8.
+template <int D>
+struct MmaGeo {
+    static constexpr int CH = D / 64;                      // 128-byte chunks of a row
+    static constexpr int HEAD = CH * kTile * 128;          // one head's rows of a tile
+    static constexpr int STAGE_BYTES = 4 * HEAD;
+    static constexpr int WARPS = D == 64 ? 12 : 6;
+    static constexpr int STAGES = kRingBudget / (WARPS * STAGE_BYTES);
+    static constexpr int KS = D / 16, NB = 2 * D / 16;     // k-steps of S, 16-column blocks of O
+    static constexpr int SMEM = 1024 + WARPS * STAGES * (STAGE_BYTES + 12);
+    static_assert(STAGES >= 2 && SMEM <= 215 * 1024, "CTA does not fit an SM");
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x as three bf16 parts: x = part[0] + part[1] + part[2] to 2^-24.
+__device__ __forceinline__ void split3(float x, float (&part)[3]) {
+    part[0] = __bfloat162float(__float2bfloat16_rn(x));
+    const float r = x - part[0];
+    part[1] = __bfloat162float(__float2bfloat16_rn(r));
+    part[2] = r - part[1];
+}
+
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 8 x 8 transpose: in, lane 4 g + t holds columns 2t, 2t + 1 of row g; out, rows 2t,
+// 2t + 1 of column g.
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void add2(float* to, const float* x) {
+    const float2 r = __fadd2_rn(make_float2(to[0], to[1]), make_float2(x[0], x[1]));
+    to[0] = r.x, to[1] = r.y;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(MmaGeo<D>::WARPS * 32, 1)
+differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv) {
+    using M = MmaGeo<D>;
+    constexpr int QB = R <= 2 ? 1 : R == 4 ? 2 : D == 128 ? 2 : 3;   // products of S (B operands of Q)
+    constexpr int SETS = R == 8 ? 2 : 1;        // accumulators of O
+    constexpr int NC = R <= 2 ? 1 : R == 4 ? 2 : 4;      // (query, map) pairs of a lane
+    pdl_launch_dependents();                    // the merge grid waits for this grid's end
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Prefix prefix;
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = warp * gridDim.x + blockIdx.x;
+    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * M::STAGES;
+    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * M::STAGES;
+    if (lane == 0) {
+        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+    }
+    int stride, entries;
+    const int64_t total = build_prefix(p, prefix, stride, entries);
+    zero_empty(p, D);
+    const Share share = share_of(p, total, w);
+    if (share.n == 0) return;
+    const int n_work = share.n;
+    Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
+    Cursor prod = cur;
+    Pager pager;
+    int64_t f = share.begin;
+    const uint64_t policy = l2_stream_policy();
+    const int tpp = p.P / kTile;
+
+    auto issue = [&](int s) {
+        const int gt = prod.tile0 + prod.tile;
+        const int pi = gt / tpp;
+        const int32_t page = pager.page(p, prod, pi);
+        if (lane == 0) {
+            stage_page[s] = page;
+            if (page < 0 || page >= p.n_pages) {
+                atomicOr(p.err, PKV_DEVERR_PAGE_ID);
+                mbar_arrive(&bars[s]);
+            } else {
+                const int h = prod.ln / p.subs, slot = (gt - pi * tpp) * kTile;
+                unsigned char* dst = ring + s * M::STAGE_BYTES;
+                mbar_arrive_expect_tx(&bars[s], M::STAGE_BYTES);
+                tma_load_5d(dst, &tmk, 0, slot, 0, 2 * h, page, &bars[s], policy);
+                tma_load_5d(dst + 2 * M::HEAD, &tmv, 0, slot, 0, 2 * h, page, &bars[s], policy);
+            }
+        }
+        cursor_next(p, prod);
+    };
+    int issued = n_work < M::STAGES ? n_work : M::STAGES;
+    for (int s = 0; s < issued; ++s) issue(s);
+
+    const int g = lane >> 2, t = lane & 3;          // fragment row, column pair
+    const int mj = lane >> 3, mr = lane & 7;        // ldmatrix: matrix and row of this address
+    // inside a stage, chunk c (16 bytes) of key row `key` is at
+    // (c / 8) * 2048 + key * 128 + ((c % 8) ^ (key % 8)) * 16, heads HEAD apart
+    const uint32_t k_row = (uint32_t)((((mj & 1) << 3) + mr) * 128);
+    const uint32_t v_row = (uint32_t)((((mj >> 1) << 3) + mr) * 128) + 2 * M::HEAD;
+    // combo i of this lane: query row and map
+    auto combo_row = [&](int i) { return R == 1 ? 0 : R == 2 ? t >> 1 : R == 4 ? t : 2 * t + (i & 1); };
+    auto combo_map = [&](int i) { return R == 1 ? t >> 1 : R == 2 ? t & 1 : R == 4 ? i : i >> 1; };
+    uint32_t qb[2][M::KS][QB][2];
+    float o[SETS][M::NB][4];
+    float m[NC], l[NC];
+    bool has_start = false;
+    LaneRows L{};
+    int s = 0;
+    uint32_t parity = 0;
+
+    for (int k = 0; k < n_work; ++k, ++f) {
+        if (k == 0 || cur.tile == 0) {              // a new lane piece
+            has_start = cur.tile == 0;
+            L = lane_rows(p, cur.x, cur.ln);
+            // B operand column g: this lane's query and part of it
+            const int qr = R == 1 ? 0 : R == 2 ? g >> 2 : R == 4 ? g >> 1 : g;
+            int64_t row;
+            int head, st, en;
+            const bool ok = row_at(p, L, qr, row, head, st, en);
+#pragma unroll
+            for (int mm = 0; mm < 2; ++mm) {
+                const float* q = static_cast<const float*>(p.q) + (row * 2 + mm) * D + 2 * t;
+#pragma unroll
+                for (int ks = 0; ks < M::KS; ++ks) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2 x = make_float2(0.f, 0.f);
+                        if (ok) x = *reinterpret_cast<const float2*>(q + ks * 16 + 8 * i);
+                        float a[3], b[3];
+                        split3(x.x * p.qscale, a);
+                        split3(x.y * p.qscale, b);
+#pragma unroll
+                        for (int u = 0; u < QB; ++u) {
+                            // parts: R <= 2 g % 4, R = 4 (hi, mid) then (lo, 0), R = 8 part u
+                            const int part = R <= 2 ? g & 3 : R == 4 ? 2 * u + (g & 1) : u;
+                            const float xa = part == 0 ? a[0] : part == 1 ? a[1] : part == 2 ? a[2] : 0.f;
+                            const float xb = part == 0 ? b[0] : part == 1 ? b[1] : part == 2 ? b[2] : 0.f;
+                            qb[mm][ks][u][i] = pack(xa, xb);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < SETS; ++u)
+#pragma unroll
+                for (int nb = 0; nb < M::NB; ++nb)
+                    o[u][nb][0] = o[u][nb][1] = o[u][nb][2] = o[u][nb][3] = 0.f;
+        }
+        if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
+            give_up(p, bars, M::STAGES, s, parity, issued - k);
+            return;
+        }
+        unsigned char* stage = ring + s * M::STAGE_BYTES;
+        const int k0 = (cur.tile0 + cur.tile) * kTile;
+        const int32_t page = stage_page[s];
+        if (page >= 0 && page < p.n_pages) {
+            const int lo = first_pos(p, L.t, L.nt);
+            const bool edge = k0 < lo || k0 + kTile > L.t;
+            if (edge) {
+                // value rows that no query of the lane reads may hold anything: zeros, so that
+                // a weight of 0 times them is 0
+                for (int i = lane; i < kTile * 2 * M::CH * 8; i += 32) {
+                    const int rw = (i >> 3) % kTile;
+                    if (k0 + rw < lo || k0 + rw >= L.t)
+                        *reinterpret_cast<uint4*>(stage + 2 * M::HEAD + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            if (p.k_new != nullptr && L.t - 1 >= k0 && L.t - 1 < k0 + kTile) {
+                // the new token's rows: into the staged tile and into the page
+                const int slot = L.t - 1 - k0;
+                const int64_t src = ((int64_t)cur.x * 2 * p.Hp + 2 * L.h) * D;
+                const int64_t dst = (((int64_t)page * 2 * p.Hp + 2 * L.h) * p.P + (L.t - 1) % p.P) * D;
+                constexpr int PIECES = 2 * D / 8;   // of both heads' rows
+                for (int i = lane; i < 2 * PIECES; i += 32) {
+                    const bool value = i >= PIECES;
+                    const int c = value ? i - PIECES : i, hd = c / (D / 8), cc = c - hd * (D / 8);
+                    const uint4 x = *reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(value ? p.v_new : p.k_new) + src + c * 8);
+                    *reinterpret_cast<uint4*>(stage + (value ? 2 : 0) * M::HEAD + hd * M::HEAD +
+                                              (cc >> 3) * kTile * 128 + slot * 128 +
+                                              (((cc & 7) ^ (slot & 7)) << 4)) = x;
+                    if (L.sub == 0)
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(value ? p.v_pages : p.k_pages) +
+                                                  dst + (int64_t)hd * p.P * D + cc * 8) = x;
+                }
+                __syncwarp();
+            }
+            const uint32_t base = smem_u32(stage);
+            float sm[2][4];                         // S of map 0, 1: keys g, g + 8
+#pragma unroll
+            for (int mm = 0; mm < 2; ++mm) {
+                float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < M::KS; ++ks) {
+                    // matrices: (keys 0-7, chunk 2ks), (keys 8-15, 2ks), then chunk 2ks + 1
+                    const int c = 2 * ks;
+                    uint32_t kf[4];
+                    ldsm_x4(base + mm * M::HEAD + (c >> 3) * (kTile * 128) + k_row +
+                                ((((c & 7) + (mj >> 1)) ^ mr) << 4), kf);
+#pragma unroll
+                    for (int u = 0; u < QB; ++u) mma_bf16(ks & 1 ? b : a, kf, qb[mm][ks][u][0], qb[mm][ks][u][1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sm[mm][i] = a[i] + b[i];
+            }
+            float sc[NC][2];                        // scores of the lane's combos at keys g, g + 8
+            if constexpr (R <= 2) {
+                // both lanes of a pair get hi + mid + lo of their query
+#pragma unroll
+                for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = sm[mm][2 * i] + sm[mm][2 * i + 1];
+                        sm[mm][i] = x + __shfl_xor_sync(0xffffffffu, x, 1);
+                    }
+                const bool second = combo_map(0) != 0;
+                sc[0][0] = second ? sm[1][0] : sm[0][0];
+                sc[0][1] = second ? sm[1][1] : sm[0][1];
+            } else if constexpr (R == 4) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    sc[i][0] = sm[i][0] + sm[i][1], sc[i][1] = sm[i][2] + sm[i][3];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[i][0] = sm[i >> 1][i & 1], sc[i][1] = sm[i >> 1][2 + (i & 1)];
+            }
+            if (edge || L.nt > 1) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    int64_t row;
+                    int head, st, en;
+                    if (!row_at(p, L, combo_row(i), row, head, st, en)) en = 0;
+                    if (k0 + g < st || k0 + g >= en) sc[i][0] = -INFINITY;
+                    if (k0 + 8 + g < st || k0 + 8 + g >= en) sc[i][1] = -INFINITY;
+                }
+            }
+            float alpha[NC], pr[NC][2];
+            bool moved = false;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float mx = fmaxf(sc[i][0], sc[i][1]);
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                alpha[i] = 1.f;
+                if (mx > m[i] + 8.f || (m[i] == -INFINITY && mx > m[i])) {
+                    alpha[i] = exp2f(m[i] - mx);    // 0 for the first
+                    m[i] = mx;
+                    l[i] *= alpha[i];
+                    moved = true;
+                }
+                const float mb = m[i] == -INFINITY ? 0.f : m[i];
+                pr[i][0] = exp2f(sc[i][0] - mb), pr[i][1] = exp2f(sc[i][1] - mb);
+                l[i] += pr[i][0] + pr[i][1];
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int u = 0; u < SETS; ++u) {
+                    const float a0 = alpha[R == 8 ? 2 * u : 0], a1 = alpha[R <= 2 ? 0 : 2 * u + 1];
+#pragma unroll
+                    for (int nb = 0; nb < M::NB; ++nb) {
+                        o[u][nb][0] *= a0, o[u][nb][1] *= a1;
+                        o[u][nb][2] *= a0, o[u][nb][3] *= a1;
+                    }
+                }
+            }
+            // B operands of O: keys 0-7 and 8-15, transposed; smallest parts first
+            constexpr int PB = R == 1 ? 1 : R == 2 ? 2 : 3;
+            uint32_t pb[SETS][PB][2];
+            float part[NC][2][3];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                split3(pr[i][0], part[i][0]);
+                split3(pr[i][1], part[i][1]);
+            }
+#pragma unroll
+            for (int u = 0; u < SETS; ++u)
+#pragma unroll
+                for (int v = 0; v < PB; ++v)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float* x = part[R == 8 ? 2 * u : 0][i];
+                        const float* y = part[R <= 2 ? 0 : 2 * u + 1][i];
+                        uint32_t z;
+                        if constexpr (R == 1) z = t & 1 ? pack(x[2], 0.f) : pack(x[0], x[1]);
+                        else if constexpr (R == 2) z = v == 0 ? pack(x[2], 0.f) : pack(x[0], x[1]);
+                        else z = pack(x[2 - v], y[2 - v]);
+                        pb[u][v][i] = transpose(z);
+                    }
+#pragma unroll
+            for (int nb = 0; nb < M::NB; ++nb) {
+                // matrices: (keys 0-7, chunk 2nb), (keys 0-7, 2nb + 1), then keys 8-15
+                constexpr int per = D / 8;          // chunks of one head's row
+                const int hd = 2 * nb / per, c = 2 * nb - hd * per;
+                uint32_t vf[4];
+                ldsm_x4_trans(base + hd * M::HEAD + (c >> 3) * (kTile * 128) + v_row +
+                                  ((((c & 7) + (mj & 1)) ^ mr) << 4), vf);
+#pragma unroll
+                for (int u = 0; u < SETS; ++u) {
+                    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int v = 0; v < PB; ++v) mma_bf16(a, vf, pb[u][v][0], pb[u][v][1]);
+                    add2(o[u][nb], a);
+                    add2(o[u][nb] + 2, a + 2);
+                }
+            }
+        }
+        // the stage is free again: hand it to the copy engine
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (issued < n_work) {
+            issue(s);
+            ++issued;
+        }
+        if (++s == M::STAGES) {
+            s = 0;
+            parity ^= 1u;
+        }
+
+        const bool has_end = cur.tile == cur.n - 1;
+        if (has_end || k == n_work - 1) {           // the piece ends
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+            if constexpr (R <= 2) {
+                // columns 2t, 2t + 1 are parts of one value (R = 1: of lanes t, t ^ 1 too)
+#pragma unroll
+                for (int nb = 0; nb < M::NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = o[0][nb][2 * i] + o[0][nb][2 * i + 1];
+                        if constexpr (R == 1) x += __shfl_xor_sync(0xffffffffu, x, 1);
+                        o[0][nb][i] = x;
+                    }
+            }
+            // value column nb * 16 + g + 8 i of combo c
+            auto value = [&](int c, int nb, int i) {
+                return R <= 2 ? o[0][nb][i] : o[R == 8 ? c >> 1 : 0][nb][2 * i + (c & 1)];
+            };
+            if (has_start && has_end) {
+                constexpr int NQ = R == 8 ? 2 : 1;  // queries of a lane
+#pragma unroll
+                for (int qi = 0; qi < NQ; ++qi) {
+                    int64_t row;
+                    int head, st, en;
+                    const bool ok = row_at(p, L, combo_row(qi), row, head, st, en);
+                    const float lam = ok ? __ldg(p.lambda + head) : 0.f;
+                    const int c0 = qi, c1 = R == 8 ? 2 + qi : R == 4 ? 1 : 0;    // combos of map 0, 1
+                    float d[M::NB][2], sq = 0.f;
+                    // R <= 2: the other map is in another lane
+                    constexpr int other = R == 1 ? 2 : 1;
+                    const bool second = R <= 2 && combo_map(0) != 0;
+                    const float mine = R > 2 ? 0.f : l[0] > 0.f ? (second ? -lam : 1.f) / l[0] : 0.f;
+                    const float i0 = l[c0] > 0.f ? 1.f / l[c0] : 0.f;
+                    const float i1 = l[c1] > 0.f ? lam / l[c1] : 0.f;
+#pragma unroll
+                    for (int nb = 0; nb < M::NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (R <= 2) {
+                                const float x = value(0, nb, i) * mine;
+                                d[nb][i] = x + __shfl_xor_sync(0xffffffffu, x, other);
+                            } else {
+                                d[nb][i] = value(c0, nb, i) * i0 - value(c1, nb, i) * i1;
+                            }
+                            sq = fmaf(d[nb][i], d[nb][i], sq);
+                        }
+#pragma unroll
+                    for (int x = 4; x <= 16; x <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, x);
+                    float c = p.out_scale;
+                    if (p.normalise) c *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
+                    if (!ok) continue;
+                    const bool weighted = p.normalise && p.norm_weight != nullptr;
+                    if (R == 1 && t >= 2) continue; // lanes 0, 1 hold all of it
+                    float* op = p.out + row * 2 * D;
+                    auto store = [&](int col, float x) {
+                        op[col] = x * c * (weighted ? __ldg(p.norm_weight + col) : 1.f);
+                    };
+#pragma unroll
+                    for (int nb = 0; nb < M::NB; ++nb) {
+                        if constexpr (R <= 2) {
+                            // two lanes hold the same values: one column of each block each
+                            store(nb * 16 + g + 8 * (t & 1), t & 1 ? d[nb][1] : d[nb][0]);
+                        } else {
+                            store(nb * 16 + g, d[nb][0]);
+                            store(nb * 16 + g + 8, d[nb][1]);
+                        }
+                    }
+                }
+            } else {
+                const int slot = 2 * w + (has_start ? 1 : 0);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const int r = combo_row(i), mm = combo_map(i);
+                    const int64_t at = ((int64_t)slot * R + r) * 2 + mm;
+                    if (g == 0 && (R > 1 || (t & 1) == 0)) p.part_ml[at] = make_float2(m[i], l[i]);
+                    float* po = p.part_o + at * 2 * D + g;
+#pragma unroll
+                    for (int nb = 0; nb < M::NB; ++nb) {
+                        const float x = value(i, nb, 0), y = value(i, nb, 1);
+                        if constexpr (R == 1) {
+                            po[nb * 16 + 8 * (t & 1)] = t & 1 ? y : x;
+                        } else {
+                            po[nb * 16] = x;
+                            po[nb * 16 + 8] = y;
+                        }
+                    }
+                }
+                if (has_start && lane == 0)
+                    p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, f - cur.tile + cur.n), 1);
             }
         }
         cursor_next(p, cur);
@@ -841,21 +1342,19 @@ cudaError_t configure(K kernel, int bytes, bool* done) {
     return e;
 }
 
-// Rows of one lane for G query pairs per KV pair.
-int core_rows(int dtype, int D, int G) {
-    if (D != 64 && D != 128) return 1;
-    return G >= 4 ? 4 : G;
-}
+// bf16 at head width 64 and 128 runs on the tensor cores.
+bool use_mma(int dtype, int D) { return dtype == PKV_BF16 && (D == 64 || D == 128); }
 
-// All instantiations: f(T, D, R).
+// Most query rows of one lane.
+int most_rows(int dtype, int D) { return use_mma(dtype, D) ? 8 : D == 64 || D == 128 ? 4 : 1; }
+
+// CUDA-core instantiations: f(T, D, R).
 #define PKV_DF_CORE(F)                                                                    \
     F(float, 2, 1) F(float, 4, 1) F(float, 8, 1) F(float, 16, 1) F(float, 32, 1)           \
     F(float, 64, 1) F(float, 64, 2) F(float, 64, 4)                                       \
     F(float, 128, 1) F(float, 128, 2) F(float, 128, 4)                                    \
     F(__nv_bfloat16, 2, 1) F(__nv_bfloat16, 4, 1) F(__nv_bfloat16, 8, 1)                  \
-    F(__nv_bfloat16, 16, 1) F(__nv_bfloat16, 32, 1) F(__nv_bfloat16, 256, 1)              \
-    F(__nv_bfloat16, 64, 1) F(__nv_bfloat16, 64, 2) F(__nv_bfloat16, 64, 4)               \
-    F(__nv_bfloat16, 128, 1) F(__nv_bfloat16, 128, 2) F(__nv_bfloat16, 128, 4)
+    F(__nv_bfloat16, 16, 1) F(__nv_bfloat16, 32, 1) F(__nv_bfloat16, 256, 1)
 
 template <typename T, int D, int R>
 cudaError_t launch_core(const DfParams& p, int sms, cudaStream_t stream) {
@@ -868,19 +1367,51 @@ cudaError_t launch_core(const DfParams& p, int sms, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <int D, int R>
+cudaError_t launch_mma(const DfParams& p, const void* tmap_k, const void* tmap_v, int sms,
+                       cudaStream_t stream) {
+    using M = MmaGeo<D>;
+    static bool done[64] = {};
+    cudaError_t e = configure(differential_mma_kernel<D, R>, M::SMEM, done);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmk, tmv;
+    std::memcpy(&tmk, tmap_k, sizeof tmk);
+    std::memcpy(&tmv, tmap_v, sizeof tmv);
+    const int grid = p.W < sms ? p.W : sms;
+    differential_mma_kernel<D, R><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p, tmk, tmv);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_mma_rows(const DfParams& p, const void* tmap_k, const void* tmap_v, int sms,
+                            cudaStream_t stream) {
+    switch (p.R) {
+        case 1: return launch_mma<D, 1>(p, tmap_k, tmap_v, sms, stream);
+        case 2: return launch_mma<D, 2>(p, tmap_k, tmap_v, sms, stream);
+        case 4: return launch_mma<D, 4>(p, tmap_k, tmap_v, sms, stream);
+        case 8: return launch_mma<D, 8>(p, tmap_k, tmap_v, sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-int differential_rows(int dtype, int D, int G) { return core_rows(dtype, D, G); }
+bool differential_needs_maps(int dtype, int D) { return use_mma(dtype, D); }
+
+int differential_rows(int dtype, int D, int G) {
+    const int most = most_rows(dtype, D);
+    return G < most ? G : most;
+}
 
 int differential_block_tokens(int dtype, int D, int G) {
-    const int most = core_rows(dtype, D, 128);
+    const int most = most_rows(dtype, D);
     return G <= most ? most / G : 1;
 }
 
 int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes, int64_t max_len) {
-    int warps = 0;
+    int warps = use_mma(dtype, D) ? (D == 64 ? MmaGeo<64>::WARPS : MmaGeo<128>::WARPS) : 0;
 #define PKV_DF_WARPS(T, DD, RR) \
     if (dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && D == DD && rows == RR) warps = CoreGeo<T, DD, RR>::WARPS;
     PKV_DF_CORE(PKV_DF_WARPS)
@@ -941,6 +1472,9 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
     p.part_o = reinterpret_cast<float*>(ws + L.part_o);
     if (a.ev_before) cudaEventRecord(a.ev_before, stream);
     cudaError_t e = cudaErrorInvalidValue;
+    if (use_mma(a.dtype, a.D))
+        e = a.D == 64 ? launch_mma_rows<64>(p, a.tmap_k, a.tmap_v, a.sms, stream)
+                      : launch_mma_rows<128>(p, a.tmap_k, a.tmap_v, a.sms, stream);
 #define PKV_DF_LAUNCH(T, DD, RR)                                                              \
     if (a.dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && a.D == DD && a.rows == RR)        \
         e = launch_core<T, DD, RR>(p, a.sms, stream);

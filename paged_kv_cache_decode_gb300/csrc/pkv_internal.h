@@ -286,6 +286,8 @@ struct DifferentialArgs {
     pkv_differential diff;
     float* out;                 // [tokens][(H / 2) * G][2 D]
     void* workspace;
+    const void* tmap_k;         // the layer's 5-D CUtensorMaps (host memory) where
+    const void* tmap_v;         //   differential_needs_maps
     int rows;                   // query rows of one lane (differential_rows)
     int workers;                // differential_workers
     int sms;
@@ -304,6 +306,10 @@ struct DifferentialChunkLayout {
     int64_t blocks;
     size_t rows, lens, tok0, ntok, first, total;
 };
+
+// The decode kernel loads through tensor maps of the pool as [pages][H][D/64][P][64],
+// boxes of 2 heads x 16 positions, 128-byte swizzle (bf16, head width 64 or 128).
+bool differential_needs_maps(int dtype, int D);
 
 // Query rows that share one pass over a lane's keys, for G query pairs per KV pair.
 int differential_rows(int dtype, int D, int G);

@@ -90,6 +90,8 @@ struct pkv_pool {
     bool differential = false;         // requests carry the differential calls' scratch
     std::vector<CUtensorMap> tmap_k;   // per layer, when tmaps
     std::vector<CUtensorMap> tmap_v;
+    std::vector<CUtensorMap> pair_k;   // per layer, for the differential decode (bf16, 64 / 128)
+    std::vector<CUtensorMap> pair_v;
     // failure injection (pkv_pool_inject_fault), each hook one-shot
     int64_t inject_lease = 0;          // > 0: page leases until the one that fails
     int inject_layer = -1;             // >= 0: the next layer call on this layer fails
@@ -251,6 +253,22 @@ bool encode_pool_map(CUtensorMap* map, void* base, int64_t rows, int D, int dtyp
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// One layer's K or V pool of bf16 heads as [pages][H][D/64][P][64], read in boxes of
+// one page's 16 positions x all of D x 2 heads with the 128-byte swizzle.
+bool encode_pair_map(CUtensorMap* map, void* base, const pkv_pool* p) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t row = (cuuint64_t)p->head_dim * 2;
+    cuuint64_t dims[5] = {64, (cuuint64_t)p->page_size, (cuuint64_t)(p->head_dim / 64), (cuuint64_t)p->heads,
+                          (cuuint64_t)p->pages};
+    cuuint64_t strides[4] = {row, 128, row * p->page_size, row * p->page_size * p->heads};
+    cuuint32_t box[5] = {64, (cuuint32_t)pkv::kTile, (cuuint32_t)(p->head_dim / 64), 2, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---- differential calls --------------------------------------------------------
 
 int diff_rows(const pkv_pool* p) { return pkv::differential_rows(p->dtype, p->head_dim, p->group); }
@@ -316,6 +334,10 @@ pkv::DifferentialArgs diff_args(pkv_pool* p, int layer, const pkv_differential* 
     a.n_pages = p->pages;
     a.block_tokens = 1;
     a.diff = *d;
+    if (!p->pair_k.empty()) {
+        a.tmap_k = &p->pair_k[(size_t)layer];
+        a.tmap_v = &p->pair_v[(size_t)layer];
+    }
     a.rows = diff_rows(p);
     a.sms = p->sms;
     a.dev_error = p->dev_error;
@@ -581,6 +603,23 @@ int pkv_pool_create_ex(const pkv_pool_options* opts, pkv_pool** out) {
                     delete p;
                     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for layer %d", l);
                 }
+            }
+        }
+        if (p->differential && pkv::differential_needs_maps(dtype, head_dim)) {
+            bool ok_maps = p->tmaps;
+            p->pair_k.resize((size_t)layers);
+            p->pair_v.resize((size_t)layers);
+            for (int l = 0; ok_maps && l < layers; ++l)
+                ok_maps = encode_pair_map(&p->pair_k[(size_t)l],
+                                          static_cast<char*>(p->k_base) + p->layer_bytes * (size_t)l, p) &&
+                          encode_pair_map(&p->pair_v[(size_t)l],
+                                          static_cast<char*>(p->v_base) + p->layer_bytes * (size_t)l, p);
+            if (!ok_maps) {
+                cudaFree(p->k_base);
+                cudaFree(p->v_base);
+                cudaFree(p->dev_error);
+                delete p;
+                return fail(PKV_ERR_CUDA, "tensor maps of the differential calls");
             }
         }
         // load the fixed scratch array of pkv_paged_decode_attention_static on this
