@@ -63,15 +63,41 @@ def _dtype_code(dtype) -> int:
     raise ValueError(f"unsupported storage dtype {dtype!r}")
 
 
-def _stream_ptr(stream) -> ctypes.c_void_p:
+def _stream_ptr(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _dev(t: torch.Tensor, name: str, dtype, shape) -> ctypes.c_void_p:
+def _scratch(n: int, device, stream):
+    """n bytes of scratch for one call, or None: from PyTorch's allocator each time, so that
+    calls on two streams, and a captured graph and an eager call, never share it."""
+    if n == 0:
+        return None
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    _used_on(t, stream)
+    return t
+
+
+def _workspace(t):
+    """(address, bytes) of a scratch tensor or None."""
+    return (None, 0) if t is None else (_dev(t, "workspace", torch.uint8, None), t.numel())
+
+
+def _used_on(t: torch.Tensor, stream) -> None:
+    """Tell the allocator that `t`, made on the current stream, is used on `stream`."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(stream)
+
+
+def _dev(t: torch.Tensor, name: str, dtype, shape) -> int:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -82,7 +108,7 @@ def _dev(t: torch.Tensor, name: str, dtype, shape) -> ctypes.c_void_p:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 class _DeviceArray:
@@ -107,17 +133,18 @@ class Differential:
         if norm_weight is not None:
             _dev(norm_weight, "norm_weight", torch.float32, (norm_weight.numel(),))
         self.lam, self.norm_weight = lam, norm_weight
+        self._heads = lam.numel()
+        self._width = None if norm_weight is None else norm_weight.numel()
         self._c = pkv_differential(lam.data_ptr(),
                                    None if norm_weight is None else norm_weight.data_ptr(),
                                    int(bool(normalise)), norm_eps, out_scale)
 
     def _for(self, pool: "Pool"):
         """The C struct, its sizes checked against the pool's heads."""
-        if self.lam.numel() != pool.query_heads // 2:
-            raise ValueError(f"lam must have {pool.query_heads // 2} elements, got {self.lam.numel()}")
-        if self.norm_weight is not None and self.norm_weight.numel() != 2 * pool.head_dim:
-            raise ValueError(f"norm_weight must have {2 * pool.head_dim} elements, "
-                             f"got {self.norm_weight.numel()}")
+        if self._heads != pool.query_heads // 2:
+            raise ValueError(f"lam must have {pool.query_heads // 2} elements, got {self._heads}")
+        if self._width not in (None, 2 * pool.head_dim):
+            raise ValueError(f"norm_weight must have {2 * pool.head_dim} elements, got {self._width}")
         return ctypes.byref(self._c)
 
 
@@ -156,6 +183,7 @@ class Pool:
         self.max_pages_per_request = -(-max_context // page_size)
         self._requests = []
         self._ws = {}
+        self._ws_bytes = {}     # scratch sizes of the differential calls
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -349,12 +377,12 @@ class Pool:
         oshape = (B, HQ // 2, 2 * D)
         if out is None:
             out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+            _used_on(out, stream)
         if workspace is None:
-            key = ("differential", B, max_seq_len)
-            if key not in self._ws:
-                n = self.differential_workspace_size(B, max_seq_len)
-                self._ws[key] = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-            workspace = self._ws[key]
+            n = self._ws_bytes.get((B, max_seq_len))
+            if n is None:
+                n = self._ws_bytes[(B, max_seq_len)] = self.differential_workspace_size(B, max_seq_len)
+            workspace = _scratch(n, q.device, stream)
         if page_tables.dim() != 2 or page_tables.shape[0] != B:
             raise ValueError("page_tables must be [batch, max_pages]")
         check(lib.pkv_paged_differential_decode(
@@ -364,8 +392,7 @@ class Pool:
             _dev(v_new, "v_new", self.torch_dtype, (B, H, D)),
             _dev(page_tables, "page_tables", torch.int32, None), page_tables.shape[1],
             _dev(seq_lens, "seq_lens", torch.int32, (B,)), int(max_seq_len), diff._for(self),
-            _dev(out, "out", torch.float32, oshape),
-            _dev(workspace, "workspace", torch.uint8, None), workspace.numel(),
+            _dev(out, "out", torch.float32, oshape), *_workspace(workspace),
             _stream_ptr(stream)), "pkv_paged_differential_decode")
         return out
 
@@ -384,12 +411,12 @@ class Pool:
         oshape = (N, HQ // 2, 2 * D)
         if out is None:
             out = torch.empty(oshape, dtype=torch.float32, device=q.device)
+            _used_on(out, stream)
         if workspace is None:
-            key = ("differential_prefill", B, N)
-            if key not in self._ws:
-                n = self.differential_prefill_workspace_size(B, N)
-                self._ws[key] = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-            workspace = self._ws[key]
+            n = self._ws_bytes.get(("prefill", B, N))
+            if n is None:
+                n = self._ws_bytes[("prefill", B, N)] = self.differential_prefill_workspace_size(B, N)
+            workspace = _scratch(n, q.device, stream)
         if page_tables.dim() != 2 or page_tables.shape[0] != B:
             raise ValueError("page_tables must be [batch, max_pages]")
         check(lib.pkv_paged_differential_prefill(
@@ -400,8 +427,7 @@ class Pool:
             _dev(cu_new, "cu_new", torch.int32, (B + 1,)),
             _dev(page_tables, "page_tables", torch.int32, None), page_tables.shape[1],
             _dev(seq_lens, "seq_lens", torch.int32, (B,)), diff._for(self),
-            _dev(out, "out", torch.float32, oshape),
-            _dev(workspace, "workspace", torch.uint8, None), workspace.numel(),
+            _dev(out, "out", torch.float32, oshape), *_workspace(workspace),
             _stream_ptr(stream)), "pkv_paged_differential_prefill")
         return out
 

@@ -50,8 +50,11 @@ namespace pkv {
 namespace {
 
 constexpr uint64_t kWaitNs = 4000000000ull;     // 4 s per bounded wait
-constexpr int kPrefix = 1024;                   // entries of the tile prefix in shared memory
+constexpr int kPrefix = 512;                    // entries of the tile prefix in shared memory
 constexpr int kRingBudget = 196608;             // stage-ring bytes of one CTA (one CTA per SM)
+// What a lane costs beside its tiles, in tiles.  64 requests of up to 4096 positions, 16 KV
+// pairs: 343 us at 1, 337 at 2, 331 at 4; short windows (64 tiles a lane): 37.7, 36.5, 37.0.
+constexpr int kLaneCost = 3;
 
 struct DfParams {
     const void* q;              // [token][2 * Hp * G][D], fp32 or (q_bf16) bf16
@@ -70,6 +73,7 @@ struct DfParams {
     const int32_t* tok0;        // prefill blocks: first chunk row and token count of block x
     const int32_t* ntok;        //   (nullptr: one token, row x)
     int B, Hp, G, subs, P;      // subs: row blocks per (request, pair)
+    int tile;                   // positions of a tile (16, or 8)
     int64_t window;
     float qscale;               // log2(e) / sqrt(D)
     const float* lambda;        // [Hp * G]
@@ -109,11 +113,19 @@ __device__ __forceinline__ bool len_ok(const DfParams& p, int t) {
 __device__ __forceinline__ int tiles_at(const DfParams& p, int x) {
     const int t = len_at(p, x);
     if (t <= 0 || !len_ok(p, t)) return 0;
-    return (t + kTile - 1) / kTile - first_pos(p, t, ntok_at(p, x)) / kTile;
+    return (t + p.tile - 1) / p.tile - first_pos(p, t, ntok_at(p, x)) / p.tile;
 }
 
-// Tile prefix over requests, every `stride` of them, in shared memory; all threads of
-// the CTA.  pre[e] = tiles of requests below e * stride; returns the total.
+// The same in units of work: a lane is charged kLaneCost units, before its tiles, for what
+// its start and end take (queries, epilogue), so that a worker with many short lanes
+// gets fewer tiles.
+__device__ __forceinline__ int units_at(const DfParams& p, int x) {
+    const int n = tiles_at(p, x);
+    return n > 0 ? n + kLaneCost : 0;
+}
+
+// Unit prefix over requests, every `stride` of them, in shared memory; all threads of
+// the CTA.  pre[e] = units of one lane of the requests below e * stride; returns the total.
 struct Prefix {
     int64_t pre[kPrefix + 1];
     int64_t warp_sum[32];
@@ -128,7 +140,7 @@ __device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& 
     const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
     int64_t n = 0;
     for (int x = e0 * stride; x < min(e1 * stride, p.B); ++x) {
-        n += tiles_at(p, x);
+        n += units_at(p, x);
         if (blockIdx.x == 0 && !len_ok(p, len_at(p, x))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
     }
     int64_t incl = n;
@@ -147,26 +159,35 @@ __device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& 
     for (int e = e0; e < e1; ++e) {
         s.pre[e] = at;
         if (e + 1 < e1)
-            for (int x = e * stride; x < (e + 1) * stride; ++x) at += tiles_at(p, x);
+            for (int x = e * stride; x < (e + 1) * stride; ++x) at += units_at(p, x);
     }
     if (tid == 0) s.pre[entries] = total;
     __syncthreads();
     return total;
 }
 
-// A place in the flattened (request, lane, tile) sequence.
+// A place in the flattened (request, lane, unit) sequence, always at a tile.
 struct Cursor {
+    int64_t f;                  // flattened unit
     int x, ln, tile;            // request, lane of it, tile of the lane
-    int n, tile0, t;            // the request's tiles per lane, first tile, length
+    int n, tile0;               // the request's tiles per lane, first tile
+    int h, sub;                 // the lane's KV pair and row block
+    int page, slot;             // the tile's page of the request, tile of that page
 };
 
 __device__ __forceinline__ void cursor_load(const DfParams& p, Cursor& c) {
-    c.t = len_at(p, c.x);
     c.n = tiles_at(p, c.x);
-    c.tile0 = first_pos(p, c.t, ntok_at(p, c.x)) / kTile;
+    c.tile0 = first_pos(p, len_at(p, c.x), ntok_at(p, c.x)) / p.tile;
 }
 
-// Cursor at flattened tile f; *lane_start receives the flattened index of its lane.
+// Places within the pages for the cursor's tile.
+__device__ __forceinline__ void cursor_place(const DfParams& p, Cursor& c) {
+    const int gt = c.tile0 + c.tile, tpp = p.P / p.tile;
+    c.page = gt / tpp;
+    c.slot = gt - c.page * tpp;
+}
+
+// Cursor at the first tile at or behind flattened unit f.
 __device__ Cursor cursor_at(const DfParams& p, const Prefix& s, int stride, int entries, int64_t f) {
     const int LN = p.Hp * p.subs;
     int lo = 0, hi = entries - 1;               // largest e with LN * pre[e] <= f
@@ -179,27 +200,51 @@ __device__ Cursor cursor_at(const DfParams& p, const Prefix& s, int stride, int 
     Cursor c;
     c.x = lo * stride;
     for (;;) {
-        const int n = tiles_at(p, c.x);
+        const int n = units_at(p, c.x);
         if (f < base + (int64_t)LN * n || c.x == p.B - 1) break;
         base += (int64_t)LN * n;
         ++c.x;
     }
     cursor_load(p, c);
     const int64_t local = f - base;
-    c.ln = (int)(local / c.n);
-    c.tile = (int)(local - (int64_t)c.ln * c.n);
+    const int per = c.n + kLaneCost;
+    c.ln = (int)(local / per);
+    c.tile = (int)(local - (int64_t)c.ln * per) - kLaneCost;
+    c.f = f;
+    if (c.tile < 0) {
+        c.f -= c.tile;
+        c.tile = 0;
+    }
+    c.h = c.ln / p.subs;
+    c.sub = c.ln - c.h * p.subs;
+    cursor_place(p, c);
     return c;
 }
 
 __device__ __forceinline__ void cursor_next(const DfParams& p, Cursor& c) {
-    if (++c.tile < c.n) return;
+    ++c.f;
+    if (++c.tile < c.n) {
+        if (++c.slot * p.tile == p.P) {
+            c.slot = 0;
+            ++c.page;
+        }
+        return;
+    }
     c.tile = 0;
-    if (++c.ln < p.Hp * p.subs) return;
-    c.ln = 0;
-    do {
-        ++c.x;
-    } while (c.x < p.B && tiles_at(p, c.x) == 0);
-    if (c.x < p.B) cursor_load(p, c);
+    c.f += kLaneCost;
+    if (++c.sub == p.subs) {
+        c.sub = 0;
+        ++c.h;
+    }
+    if (++c.ln == p.Hp * p.subs) {
+        c.ln = c.h = c.sub = 0;
+        do {
+            ++c.x;
+        } while (c.x < p.B && tiles_at(p, c.x) == 0);
+        if (c.x >= p.B) return;
+        cursor_load(p, c);
+    }
+    cursor_place(p, c);
 }
 
 // Page ids of a cursor's tiles, 32 table entries at a time: lane i holds entry base + i.
@@ -207,7 +252,8 @@ struct Pager {
     int x = -1, base = 0;
     int32_t val = -1;
 
-    __device__ __forceinline__ int32_t page(const DfParams& p, const Cursor& c, int index) {
+    __device__ __forceinline__ int32_t page(const DfParams& p, const Cursor& c) {
+        const int index = c.page;
         if (c.x != x || index < base || index >= base + 32) {
             x = c.x;
             base = index;
@@ -219,25 +265,24 @@ struct Pager {
     }
 };
 
-// One worker's share of the flattened tiles (every worker that works has one at least).
+// One worker's share of the flattened units (every worker that works has one at least).
 struct Share {
-    int64_t all, begin;         // tiles of the launch, first of this worker
-    int workers, n;             // workers with work, tiles of this one (0: none)
+    int64_t all, begin, end;    // units of the launch, first of this worker, one past its last
+    int workers;                // workers with work
 };
 
-__device__ __forceinline__ Share share_of(const DfParams& p, int64_t requests_tiles, int w) {
+__device__ __forceinline__ Share share_of(const DfParams& p, int64_t requests_units, int w) {
     Share s;
-    s.all = (int64_t)p.Hp * p.subs * requests_tiles;
+    s.all = (int64_t)p.Hp * p.subs * requests_units;
     s.workers = (int)(s.all < p.W ? s.all : p.W);
-    s.n = 0;
-    s.begin = 0;
+    s.begin = s.end = 0;
     if (w >= s.workers) return s;
     s.begin = w * s.all / s.workers;
-    s.n = (int)((w + 1) * s.all / s.workers - s.begin);
+    s.end = (w + 1) * s.all / s.workers;
     return s;
 }
 
-// The last worker of a lane that ends before flattened tile `lane_end`: the inverse of
+// The last worker of a lane that ends before flattened unit `lane_end`: the inverse of
 // `begin` above.
 __device__ __forceinline__ int last_worker(const Share& s, int64_t lane_end) {
     return (int)((lane_end * s.workers - 1) / s.all);
@@ -266,15 +311,17 @@ __device__ __forceinline__ void give_up(const DfParams& p, uint64_t* bars, int s
 // ([token][Hp * G]), attending positions start .. end - 1.
 struct LaneRows {
     int t, nt, tok0, h, sub;
+    int lo;                     // first position any row reads
 };
 
-__device__ __forceinline__ LaneRows lane_rows(const DfParams& p, int x, int ln) {
+__device__ __forceinline__ LaneRows lane_rows(const DfParams& p, int x, int h, int sub) {
     LaneRows L;
     L.t = len_at(p, x);
     L.nt = ntok_at(p, x);
     L.tok0 = p.tok0 ? __ldg(p.tok0 + x) : x;
-    L.h = ln / p.subs;
-    L.sub = ln - L.h * p.subs;
+    L.h = h;
+    L.sub = sub;
+    L.lo = first_pos(p, L.t, L.nt);
     return L;
 }
 
@@ -288,6 +335,30 @@ __device__ __forceinline__ bool row_at(const DfParams& p, const LaneRows& L, int
     end = ok ? L.t - (L.nt - 1 - tok) : 0;
     start = (p.window > 0 && end > p.window) ? (int)(end - p.window) : 0;
     return ok;
+}
+
+// A warp, a few tiles ahead: fetch into L1 the queries that the lane at `c` starts with, or
+// the new key and value rows that it ends with.
+template <int D, int ES>
+__device__ __forceinline__ void prefetch_rows(const DfParams& p, const Cursor& c) {
+    const int lane = threadIdx.x & 31;
+    auto fetch = [](const char* at) { asm volatile("prefetch.global.L1 [%0];" ::"l"(at)); };
+    const LaneRows L = lane_rows(p, c.x, c.h, c.sub);
+    if (c.tile == 0) {
+        const int es = p.q_bf16 ? 2 : 4, per = (2 * D * es + 127) / 128;    // lines of one row
+        for (int i = lane; i < p.R * per; i += 32) {
+            int64_t row;
+            int head, st, en;
+            if (row_at(p, L, i / per, row, head, st, en))
+                fetch(static_cast<const char*>(p.q) + row * 2 * D * es + (i % per) * 128);
+        }
+    }
+    if (p.k_new != nullptr && c.tile == c.n - 1) {
+        constexpr int per = (2 * D * ES + 127) / 128;
+        const int64_t at = ((int64_t)c.x * p.Hp + L.h) * 2 * D * ES;
+        for (int i = lane; i < 2 * per; i += 32)
+            fetch(static_cast<const char*>(i < per ? p.k_new : p.v_new) + at + (i % per) * 128);
+    }
 }
 
 // ------------------------------------------------------- CUDA-core engine --
@@ -317,7 +388,10 @@ struct CoreGeo {
 template <typename T, int N>
 __device__ __forceinline__ void load_feats(const T* src, float* dst) {
     if constexpr (sizeof(T) == 4) {
-        if constexpr (N == 4) {
+        if constexpr (N == 8) {
+            load_feats<T, 4>(src, dst);
+            load_feats<T, 4>(src + 4, dst + 4);
+        } else if constexpr (N == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
             dst[0] = v.x, dst[1] = v.y, dst[2] = v.z, dst[3] = v.w;
         } else if constexpr (N == 2) {
@@ -374,27 +448,21 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
     const int64_t total = build_prefix(p, prefix, stride, entries);
     zero_empty(p, D);
     const Share share = share_of(p, total, w);
-    if (share.n == 0) return;
-    const int n_work = share.n;
+    if (share.begin == share.end) return;
     Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
+    if (cur.f >= share.end) return;
     Cursor prod = cur;
     Pager pager;
-    int64_t f = share.begin;                        // flattened index of cur
     const uint64_t policy = l2_stream_policy();
-    const int tpp = p.P / kTile;
-
     auto issue = [&](int s) {
-        const int gt = prod.tile0 + prod.tile;
-        const int pi = gt / tpp;
-        const int32_t page = pager.page(p, prod, pi);
+        const int32_t page = pager.page(p, prod);
         if (lane == 0) {
             stage_page[s] = page;
             if (page < 0 || page >= p.n_pages) {
                 atomicOr(p.err, PKV_DEVERR_PAGE_ID);
                 mbar_arrive(&bars[s]);
             } else {
-                const int h = prod.ln / p.subs;
-                const int64_t row = ((int64_t)page * 2 * p.Hp + 2 * h) * p.P + (gt - pi * tpp) * kTile;
+                const int64_t row = ((int64_t)page * 2 * p.Hp + 2 * prod.h) * p.P + prod.slot * kTile;
                 const T* k = static_cast<const T*>(p.k_pages) + row * D;
                 const T* v = static_cast<const T*>(p.v_pages) + row * D;
                 unsigned char* dst = ring + s * M::STAGE_BYTES;
@@ -405,10 +473,11 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
                 bulk_copy_g2s(dst + 3 * M::TB, v + (int64_t)p.P * D, M::TB, &bars[s], policy);
             }
         }
+        if (prod.tile == 0 || prod.tile == prod.n - 1) prefetch_rows<D, sizeof(T)>(p, prod);
         cursor_next(p, prod);
     };
-    int issued = n_work < M::STAGES ? n_work : M::STAGES;
-    for (int s = 0; s < issued; ++s) issue(s);
+    int ahead = 0;                                  // tiles staged and not yet used
+    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
 
     const bool own = lane * F < D;                  // D < 32: the lanes past D idle
     const int feat = own ? lane * F : 0;
@@ -421,25 +490,25 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
     int s = 0;
     uint32_t parity = 0;
 
-    for (int k = 0; k < n_work; ++k, ++f) {
-        if (k == 0 || cur.tile == 0) {              // a new lane piece
+    for (bool first = true; cur.f < share.end; first = false) {
+        if (first || cur.tile == 0) {               // a new lane piece
             has_start = cur.tile == 0;
-            L = lane_rows(p, cur.x, cur.ln);
+            L = lane_rows(p, cur.x, cur.h, cur.sub);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 int64_t row;
                 int head;
                 const bool ok = row_at(p, L, r, row, head, r_start[r], r_end[r]);
+                // unconditional loads, so that they overlap (a row that is none reads the
+                // lane's first)
 #pragma unroll
                 for (int mm = 0; mm < 2; ++mm) {
                     const int64_t at = (row * 2 + mm) * D + feat;
+                    if (p.q_bf16) load_feats<__nv_bfloat16, F>(static_cast<const __nv_bfloat16*>(p.q) + at, q[r][mm]);
+                    else load_feats<float, F>(static_cast<const float*>(p.q) + at, q[r][mm]);
 #pragma unroll
                     for (int i = 0; i < F; ++i) {
-                        float x = 0.f;
-                        if (ok && own)
-                            x = p.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at + i])
-                                         : static_cast<const float*>(p.q)[at + i];
-                        q[r][mm][i] = x * p.qscale;
+                        q[r][mm][i] = ok && own ? q[r][mm][i] * p.qscale : 0.f;
                         acc[r][mm][0][i] = acc[r][mm][1][i] = 0.f;
                     }
                 }
@@ -448,7 +517,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
             }
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            give_up(p, bars, M::STAGES, s, parity, issued - k);
+            give_up(p, bars, M::STAGES, s, parity, ahead);
             return;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
@@ -456,7 +525,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
         const int gt = cur.tile0 + cur.tile, k0 = gt * kTile;
         const int32_t page = stage_page[s];
         if (page >= 0 && page < p.n_pages) {
-            const int lo = first_pos(p, L.t, L.nt);
+            const int lo = L.lo;
             const bool edge = k0 < lo || k0 + kTile > L.t;
             if (edge) {
                 // rows that no query of the lane reads may hold anything: zeros, so that
@@ -563,17 +632,15 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
         // the stage is free again: hand it to the copy engine
         fence_proxy_async_smem();
         __syncwarp();
-        if (issued < n_work) {
-            issue(s);
-            ++issued;
-        }
+        if (prod.f < share.end) issue(s);
+        else --ahead;
         if (++s == M::STAGES) {
             s = 0;
             parity ^= 1u;
         }
 
         const bool has_end = cur.tile == cur.n - 1;
-        if (has_end || k == n_work - 1) {           // the piece ends
+        if (has_end || cur.f + 1 >= share.end) {    // the piece ends
             const int slot = 2 * w + (has_start ? 1 : 0);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -628,8 +695,349 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
                 }
             }
             if (has_start && !has_end && lane == 0) {
-                p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, f - cur.tile + cur.n), 1);
+                p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, cur.f - cur.tile + cur.n), 1);
             }
+        }
+        cursor_next(p, cur);
+    }
+}
+
+// ----------------------------------------------------------- fp32 engine --
+
+// fp32, head width 64 or 128, R = 1, 2 or 4 query rows a lane, CUDA cores (fp32 products
+// as they are: tensor cores would take each operand in three parts).  A stage holds a
+// tile of KT positions as TMA leaves it, K then V: [head][32-column chunk][KT rows][128
+// bytes], 128-byte swizzle (one box of a 5-D map for both heads).
+//   scores   lane (key, part): one key's dot products over D * KT / 32 features of both
+//            maps -- the swizzle spreads 8 keys' 16-byte pieces over all banks, queries
+//            come from shared memory as broadcasts -- then 5 - log2(KT) shuffles
+//   weights  one exponential a lane and row (map lane / 16), through shared memory
+//   values   a lane owns 4 or 8 of the 2 D columns for all rows and both maps: V is read
+//            once, weights as broadcasts; packed two-lane FMAs
+// KT = 8: the same ring holds twice the warps, and with several rows the kernel is bound
+// by their instruction latency (a tile of R = 4 rows is about 640 instructions).
+template <int D, int R, int KT>
+struct F32Geo {
+    static constexpr int CH = D / 32;                      // 128-byte chunks of a row
+    static constexpr int HEAD = CH * KT * 128;             // one head's rows of a tile
+    static constexpr int STAGE_BYTES = 4 * HEAD;
+    static constexpr int FIT = kRingBudget / (2 * STAGE_BYTES);
+    static constexpr int WARPS = FIT < 12 ? FIT : 12;
+    static constexpr int STAGES = kRingBudget / (WARPS * STAGE_BYTES);
+    static constexpr int PARTS = 32 / KT;                  // lanes that share a key
+    static constexpr int PIECES = D / 4 / PARTS;           // 16-byte pieces of one lane's part
+    static constexpr int NV = 2 * D / 128;                 // 4-column vectors of a lane
+    static constexpr int Q_BYTES = R * 2 * D * 4, P_BYTES = R * 2 * KT * 4;
+    static constexpr int SMEM = 1024 + WARPS * (STAGES * (STAGE_BYTES + 12) + Q_BYTES + P_BYTES);
+    static_assert(STAGES >= 2 && SMEM <= 222 * 1024, "CTA does not fit an SM");
+};
+
+__device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
+
+template <int D, int R, int KT>
+__global__ void __launch_bounds__(F32Geo<D, R, KT>::WARPS * 32, 1)
+differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constant__ CUtensorMap tmk,
+                        const __grid_constant__ CUtensorMap tmv) {
+    using M = F32Geo<D, R, KT>;
+    pdl_launch_dependents();                    // the merge grid waits for this grid's end
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Prefix prefix;
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = warp * gridDim.x + blockIdx.x;
+    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
+    float* qs = reinterpret_cast<float*>(after + warp * M::Q_BYTES);            // [R][2][D], scaled
+    float* pw = reinterpret_cast<float*>(after + M::WARPS * M::Q_BYTES + warp * M::P_BYTES);
+    after += M::WARPS * (M::Q_BYTES + M::P_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * M::STAGES;
+    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * M::STAGES;
+    if (lane == 0) {
+        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+    }
+    int stride, entries;
+    const int64_t total = build_prefix(p, prefix, stride, entries);
+    zero_empty(p, D);
+    const Share share = share_of(p, total, w);
+    if (share.begin == share.end) return;
+    Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
+    if (cur.f >= share.end) return;
+    Cursor prod = cur;
+    Pager pager;
+    const uint64_t policy = l2_stream_policy();
+    auto issue = [&](int s) {
+        const int32_t page = pager.page(p, prod);
+        if (lane == 0) {
+            stage_page[s] = page;
+            if (page < 0 || page >= p.n_pages) {
+                atomicOr(p.err, PKV_DEVERR_PAGE_ID);
+                mbar_arrive(&bars[s]);
+            } else {
+                const int slot = prod.slot * KT;
+                unsigned char* dst = ring + s * M::STAGE_BYTES;
+                mbar_arrive_expect_tx(&bars[s], M::STAGE_BYTES);
+                tma_load_5d(dst, &tmk, 0, slot, 0, 2 * prod.h, page, &bars[s], policy);
+                tma_load_5d(dst + 2 * M::HEAD, &tmv, 0, slot, 0, 2 * prod.h, page, &bars[s], policy);
+            }
+        }
+        if (prod.tile == 0 || prod.tile == prod.n - 1) prefetch_rows<D, 4>(p, prod);
+        cursor_next(p, prod);
+    };
+    int ahead = 0;                                  // tiles staged and not yet used
+    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
+
+    const int key = lane % KT, quarter = lane / KT, half = lane >> 4;
+    // 16-byte piece u of key row `key` and head hd is at hd * HEAD + (u / 8) * KT * 128 +
+    // key * 128 + ((u % 8) ^ (key % 8)) * 16
+    auto piece_at = [](int hd, int u, int row) {
+        return hd * M::HEAD + (u >> 3) * (KT * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+    };
+    float2 acc[R][2][M::NV][2];                     // [row][map][vector][column pair]
+    float m[R], l[R];                               // of this half's map
+    int r_start[R], r_end[R];
+    LaneRows L{};
+    bool has_start = false;
+    int s = 0;
+    uint32_t parity = 0;
+
+    for (bool first = true; cur.f < share.end; first = false) {
+        if (first || cur.tile == 0) {               // a new lane piece
+            has_start = cur.tile == 0;
+            L = lane_rows(p, cur.x, cur.h, cur.sub);
+            float4 x[R][2 * D / 128];
+            bool ok[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                int64_t row;
+                int head;
+                ok[r] = row_at(p, L, r, row, head, r_start[r], r_end[r]);
+                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row * 2 * D);
+#pragma unroll
+                for (int i = 0; i < 2 * D / 128; ++i) x[r][i] = __ldg(q + i * 32 + lane);
+            }
+            __syncwarp();                           // the last piece's reads of qs are done
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float c = ok[r] ? p.qscale : 0.f;
+#pragma unroll
+                for (int i = 0; i < 2 * D / 128; ++i)
+                    reinterpret_cast<float4*>(qs + r * 2 * D)[i * 32 + lane] =
+                        make_float4(x[r][i].x * c, x[r][i].y * c, x[r][i].z * c, x[r][i].w * c);
+                m[r] = -INFINITY;
+                l[r] = 0.f;
+#pragma unroll
+                for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                    for (int v = 0; v < M::NV; ++v)
+                        acc[r][mm][v][0] = acc[r][mm][v][1] = make_float2(0.f, 0.f);
+            }
+            __syncwarp();
+        }
+        if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
+            give_up(p, bars, M::STAGES, s, parity, ahead);
+            return;
+        }
+        unsigned char* stage = ring + s * M::STAGE_BYTES;
+        const int k0 = (cur.tile0 + cur.tile) * KT;
+        const int32_t page = stage_page[s];
+        if (page >= 0 && page < p.n_pages) {
+            const int lo = L.lo;
+            if (k0 < lo || k0 + KT > L.t) {
+                // value rows that no query of the lane reads may hold anything: zeros, so that
+                // a weight of 0 times them is 0
+                for (int i = lane; i < KT * 2 * M::CH * 8; i += 32) {
+                    const int rw = (i >> 3) % KT;
+                    if (k0 + rw < lo || k0 + rw >= L.t)
+                        *reinterpret_cast<uint4*>(stage + 2 * M::HEAD + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            if (p.k_new != nullptr && L.t - 1 >= k0 && L.t - 1 < k0 + KT) {
+                // the new token's rows: into the staged tile and into the page
+                const int slot = L.t - 1 - k0;
+                const int64_t src = ((int64_t)cur.x * 2 * p.Hp + 2 * L.h) * D;
+                const int64_t dst = (((int64_t)page * 2 * p.Hp + 2 * L.h) * p.P + (L.t - 1) % p.P) * D;
+                for (int i = lane; i < D; i += 32) {            // 2 x 2 rows of D / 4 pieces
+                    const bool value = i >= D / 2;
+                    const int c = value ? i - D / 2 : i, hd = c / (D / 4), u = c - hd * (D / 4);
+                    const uint4 x = *reinterpret_cast<const uint4*>(
+                        static_cast<const float*>(value ? p.v_new : p.k_new) + src + c * 4);
+                    *reinterpret_cast<uint4*>(stage + (value ? 2 : 0) * M::HEAD + piece_at(hd, u, slot)) = x;
+                    if (L.sub == 0)
+                        *reinterpret_cast<uint4*>(static_cast<float*>(value ? p.v_pages : p.k_pages) + dst +
+                                                  (int64_t)hd * p.P * D + u * 4) = x;
+                }
+                __syncwarp();
+            }
+            float sc[R];                            // this half's map, key `key`
+            {
+                float2 d[R][2];
+#pragma unroll
+                for (int mm = 0; mm < 2; ++mm) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) d[r][mm] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int u = 0; u < M::PIECES; ++u) {
+                        const int pu = quarter * M::PIECES + u;
+                        const float4 kv =
+                            *reinterpret_cast<const float4*>(stage + piece_at(mm, pu, key));
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const float4 qv =
+                                reinterpret_cast<const float4*>(qs + (r * 2 + mm) * D)[pu];
+                            d[r][mm] = __ffma2_rn(lo2(qv), lo2(kv), d[r][mm]);
+                            d[r][mm] = __ffma2_rn(hi2(qv), hi2(kv), d[r][mm]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float a = d[r][0].x + d[r][0].y, b = d[r][1].x + d[r][1].y;
+#pragma unroll
+                    for (int o = KT; o <= 8; o <<= 1) {
+                        a += __shfl_xor_sync(0xffffffffu, a, o);
+                        b += __shfl_xor_sync(0xffffffffu, b, o);
+                    }
+                    // lanes of the other half hold the rest: send them the map they want
+                    const float mine = half ? b : a, other = half ? a : b;
+                    sc[r] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+                }
+            }
+            bool moved = false;
+            float alpha[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (k0 + key < r_start[r] || k0 + key >= r_end[r]) sc[r] = -INFINITY;
+                float mx = sc[r];
+#pragma unroll
+                for (int o = 1; o < KT; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                alpha[r] = 1.f;
+                if (mx > m[r] + 8.f || (m[r] == -INFINITY && mx > m[r])) {
+                    alpha[r] = exp2f(m[r] - mx);    // 0 for the first
+                    m[r] = mx;
+                    moved = true;
+                }
+                const float pr = exp2f(sc[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                l[r] = fmaf(l[r], alpha[r], pr);
+                if (KT == 16 || (quarter & 1) == 0) pw[(r * 2 + half) * KT + key] = pr;
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float a0 = __shfl_sync(0xffffffffu, alpha[r], 0);
+                    const float a1 = __shfl_sync(0xffffffffu, alpha[r], 16);
+#pragma unroll
+                    for (int v = 0; v < M::NV; ++v)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            acc[r][0][v][i].x *= a0, acc[r][0][v][i].y *= a0;
+                            acc[r][1][v][i].x *= a1, acc[r][1][v][i].y *= a1;
+                        }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int kq = 0; kq < KT; kq += 4) {
+                float4 wt[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int mm = 0; mm < 2; ++mm)
+                        wt[r][mm] = *reinterpret_cast<const float4*>(pw + (r * 2 + mm) * KT + kq);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float4 vv[M::NV];
+#pragma unroll
+                    for (int v = 0; v < M::NV; ++v) {
+                        const int u = v * 32 + lane, hd = u / (D / 4);
+                        vv[v] = *reinterpret_cast<const float4*>(
+                            stage + 2 * M::HEAD + piece_at(hd, u - hd * (D / 4), kq + j));
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm) {
+                            const float x = (&wt[r][mm].x)[j];
+                            const float2 x2 = make_float2(x, x);
+#pragma unroll
+                            for (int v = 0; v < M::NV; ++v) {
+                                acc[r][mm][v][0] = __ffma2_rn(x2, lo2(vv[v]), acc[r][mm][v][0]);
+                                acc[r][mm][v][1] = __ffma2_rn(x2, hi2(vv[v]), acc[r][mm][v][1]);
+                            }
+                        }
+                }
+            }
+        }
+        // the stage is free again: hand it to the copy engine
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (prod.f < share.end) issue(s);
+        else --ahead;
+        if (++s == M::STAGES) {
+            s = 0;
+            parity ^= 1u;
+        }
+
+        const bool has_end = cur.tile == cur.n - 1;
+        if (has_end || cur.f + 1 >= share.end) {    // the piece ends
+            const int slot = 2 * w + (has_start ? 1 : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                int64_t row;
+                int head, st, en;
+                const bool ok = row_at(p, L, r, row, head, st, en);
+                float lt = l[r];
+#pragma unroll
+                for (int o = 1; o < KT; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+                if (has_start && has_end) {
+                    if (!ok) continue;              // alike in all lanes
+                    const float l0 = __shfl_sync(0xffffffffu, lt, 0);
+                    const float l1 = __shfl_sync(0xffffffffu, lt, 16);
+                    const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
+                    const float i1 = l1 > 0.f ? __ldg(p.lambda + head) / l1 : 0.f;
+                    float4 d[M::NV];
+                    float sq = 0.f;
+#pragma unroll
+                    for (int v = 0; v < M::NV; ++v) {
+                        const float2* a = acc[r][0][v];
+                        const float2* b = acc[r][1][v];
+                        d[v] = make_float4(a[0].x * i0 - b[0].x * i1, a[0].y * i0 - b[0].y * i1,
+                                           a[1].x * i0 - b[1].x * i1, a[1].y * i0 - b[1].y * i1);
+                        sq += d[v].x * d[v].x + d[v].y * d[v].y + d[v].z * d[v].z + d[v].w * d[v].w;
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                    float c = p.out_scale;
+                    if (p.normalise) c *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
+#pragma unroll
+                    for (int v = 0; v < M::NV; ++v) {
+                        const int col = (v * 32 + lane) * 4;
+                        float4 nw = make_float4(1.f, 1.f, 1.f, 1.f);
+                        if (p.normalise && p.norm_weight) {
+                            nw.x = __ldg(p.norm_weight + col), nw.y = __ldg(p.norm_weight + col + 1);
+                            nw.z = __ldg(p.norm_weight + col + 2), nw.w = __ldg(p.norm_weight + col + 3);
+                        }
+                        *reinterpret_cast<float4*>(p.out + row * 2 * D + col) = make_float4(
+                            d[v].x * c * nw.x, d[v].y * c * nw.y, d[v].z * c * nw.z, d[v].w * c * nw.w);
+                    }
+                } else {
+                    const int64_t at = ((int64_t)slot * R + r) * 2;
+                    if (lane % 16 == 0) p.part_ml[at + half] = make_float2(m[r], lt);
+#pragma unroll
+                    for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                        for (int v = 0; v < M::NV; ++v)
+                            *reinterpret_cast<float4*>(p.part_o + (at + mm) * 2 * D + (v * 32 + lane) * 4) =
+                                make_float4(acc[r][mm][v][0].x, acc[r][mm][v][0].y, acc[r][mm][v][1].x,
+                                            acc[r][mm][v][1].y);
+                }
+            }
+            if (has_start && !has_end && lane == 0)
+                p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, cur.f - cur.tile + cur.n), 1);
         }
         cursor_next(p, cur);
     }
@@ -743,36 +1151,32 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
     const int64_t total = build_prefix(p, prefix, stride, entries);
     zero_empty(p, D);
     const Share share = share_of(p, total, w);
-    if (share.n == 0) return;
-    const int n_work = share.n;
+    if (share.begin == share.end) return;
     Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
+    if (cur.f >= share.end) return;
     Cursor prod = cur;
     Pager pager;
-    int64_t f = share.begin;
     const uint64_t policy = l2_stream_policy();
-    const int tpp = p.P / kTile;
-
     auto issue = [&](int s) {
-        const int gt = prod.tile0 + prod.tile;
-        const int pi = gt / tpp;
-        const int32_t page = pager.page(p, prod, pi);
+        const int32_t page = pager.page(p, prod);
         if (lane == 0) {
             stage_page[s] = page;
             if (page < 0 || page >= p.n_pages) {
                 atomicOr(p.err, PKV_DEVERR_PAGE_ID);
                 mbar_arrive(&bars[s]);
             } else {
-                const int h = prod.ln / p.subs, slot = (gt - pi * tpp) * kTile;
+                const int slot = prod.slot * kTile;
                 unsigned char* dst = ring + s * M::STAGE_BYTES;
                 mbar_arrive_expect_tx(&bars[s], M::STAGE_BYTES);
-                tma_load_5d(dst, &tmk, 0, slot, 0, 2 * h, page, &bars[s], policy);
-                tma_load_5d(dst + 2 * M::HEAD, &tmv, 0, slot, 0, 2 * h, page, &bars[s], policy);
+                tma_load_5d(dst, &tmk, 0, slot, 0, 2 * prod.h, page, &bars[s], policy);
+                tma_load_5d(dst + 2 * M::HEAD, &tmv, 0, slot, 0, 2 * prod.h, page, &bars[s], policy);
             }
         }
+        if (prod.tile == 0 || prod.tile == prod.n - 1) prefetch_rows<D, sizeof(__nv_bfloat16)>(p, prod);
         cursor_next(p, prod);
     };
-    int issued = n_work < M::STAGES ? n_work : M::STAGES;
-    for (int s = 0; s < issued; ++s) issue(s);
+    int ahead = 0;                                  // tiles staged and not yet used
+    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
 
     const int g = lane >> 2, t = lane & 3;          // fragment row, column pair
     const int mj = lane >> 3, mr = lane & 7;        // ldmatrix: matrix and row of this address
@@ -791,10 +1195,10 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
     int s = 0;
     uint32_t parity = 0;
 
-    for (int k = 0; k < n_work; ++k, ++f) {
-        if (k == 0 || cur.tile == 0) {              // a new lane piece
+    for (bool first = true; cur.f < share.end; first = false) {
+        if (first || cur.tile == 0) {               // a new lane piece
             has_start = cur.tile == 0;
-            L = lane_rows(p, cur.x, cur.ln);
+            L = lane_rows(p, cur.x, cur.h, cur.sub);
             // B operand column g: this lane's query and part of it
             const int qr = R == 1 ? 0 : R == 2 ? g >> 2 : R == 4 ? g >> 1 : g;
             int64_t row;
@@ -802,16 +1206,23 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
             const bool ok = row_at(p, L, qr, row, head, st, en);
 #pragma unroll
             for (int mm = 0; mm < 2; ++mm) {
+                // all loads first: one latency, not one for each (a row that is none reads the
+                // lane's first)
                 const float* q = static_cast<const float*>(p.q) + (row * 2 + mm) * D + 2 * t;
+                const float scale = ok ? p.qscale : 0.f;
+                float2 x[M::KS][2];
+#pragma unroll
+                for (int ks = 0; ks < M::KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        x[ks][i] = *reinterpret_cast<const float2*>(q + ks * 16 + 8 * i);
 #pragma unroll
                 for (int ks = 0; ks < M::KS; ++ks) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float2 x = make_float2(0.f, 0.f);
-                        if (ok) x = *reinterpret_cast<const float2*>(q + ks * 16 + 8 * i);
                         float a[3], b[3];
-                        split3(x.x * p.qscale, a);
-                        split3(x.y * p.qscale, b);
+                        split3(x[ks][i].x * scale, a);
+                        split3(x[ks][i].y * scale, b);
 #pragma unroll
                         for (int u = 0; u < QB; ++u) {
                             // parts: R <= 2 g % 4, R = 4 (hi, mid) then (lo, 0), R = 8 part u
@@ -835,14 +1246,14 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                     o[u][nb][0] = o[u][nb][1] = o[u][nb][2] = o[u][nb][3] = 0.f;
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            give_up(p, bars, M::STAGES, s, parity, issued - k);
+            give_up(p, bars, M::STAGES, s, parity, ahead);
             return;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
         const int k0 = (cur.tile0 + cur.tile) * kTile;
         const int32_t page = stage_page[s];
         if (page >= 0 && page < p.n_pages) {
-            const int lo = first_pos(p, L.t, L.nt);
+            const int lo = L.lo;
             const bool edge = k0 < lo || k0 + kTile > L.t;
             if (edge) {
                 // value rows that no query of the lane reads may hold anything: zeros, so that
@@ -996,17 +1407,15 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
         // the stage is free again: hand it to the copy engine
         fence_proxy_async_smem();
         __syncwarp();
-        if (issued < n_work) {
-            issue(s);
-            ++issued;
-        }
+        if (prod.f < share.end) issue(s);
+        else --ahead;
         if (++s == M::STAGES) {
             s = 0;
             parity ^= 1u;
         }
 
         const bool has_end = cur.tile == cur.n - 1;
-        if (has_end || k == n_work - 1) {           // the piece ends
+        if (has_end || cur.f + 1 >= share.end) {    // the piece ends
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -1096,7 +1505,7 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                     }
                 }
                 if (has_start && lane == 0)
-                    p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, f - cur.tile + cur.n), 1);
+                    p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, cur.f - cur.tile + cur.n), 1);
             }
         }
         cursor_next(p, cur);
@@ -1119,7 +1528,7 @@ __global__ void __launch_bounds__(kMergeThreads) differential_merge_kernel(const
     const int w0 = blockIdx.x, r = blockIdx.y;
     const int4 rc = p.rec[w0];
     if (rc.w == 0) return;
-    const LaneRows L = lane_rows(p, rc.x, rc.y);
+    const LaneRows L = lane_rows(p, rc.x, rc.y / p.subs, rc.y % p.subs);
     int64_t row;
     int head, st, en;
     if (!row_at(p, L, r, row, head, st, en)) return;
@@ -1348,11 +1757,9 @@ bool use_mma(int dtype, int D) { return dtype == PKV_BF16 && (D == 64 || D == 12
 // Most query rows of one lane.
 int most_rows(int dtype, int D) { return use_mma(dtype, D) ? 8 : D == 64 || D == 128 ? 4 : 1; }
 
-// CUDA-core instantiations: f(T, D, R).
+// Other head widths, one row a lane: f(T, D, R).
 #define PKV_DF_CORE(F)                                                                    \
     F(float, 2, 1) F(float, 4, 1) F(float, 8, 1) F(float, 16, 1) F(float, 32, 1)           \
-    F(float, 64, 1) F(float, 64, 2) F(float, 64, 4)                                       \
-    F(float, 128, 1) F(float, 128, 2) F(float, 128, 4)                                    \
     F(__nv_bfloat16, 2, 1) F(__nv_bfloat16, 4, 1) F(__nv_bfloat16, 8, 1)                  \
     F(__nv_bfloat16, 16, 1) F(__nv_bfloat16, 32, 1) F(__nv_bfloat16, 256, 1)
 
@@ -1394,11 +1801,44 @@ cudaError_t launch_mma_rows(const DfParams& p, const void* tmap_k, const void* t
     }
 }
 
+// fp32 at head width 64 and 128: f(D, R, KT).
+#ifndef PKV_DF_KT64
+#define PKV_DF_KT64 16
+#endif
+#ifndef PKV_DF_KT128
+#define PKV_DF_KT128 8
+#endif
+constexpr int kTileF32_64 = PKV_DF_KT64, kTileF32_128 = PKV_DF_KT128;
+#define PKV_DF_F32(F)                                                                     \
+    F(64, 1, kTileF32_64) F(64, 2, kTileF32_64) F(64, 4, kTileF32_64)                      \
+    F(128, 1, kTileF32_128) F(128, 2, kTileF32_128) F(128, 4, kTileF32_128)
+
+int tile_of(int dtype, int D) {
+    return dtype == PKV_F32 && D == 64 ? kTileF32_64 : dtype == PKV_F32 && D == 128 ? kTileF32_128 : kTile;
+}
+
+template <int D, int R, int KT>
+cudaError_t launch_f32(const DfParams& p, const void* tmap_k, const void* tmap_v, int sms,
+                       cudaStream_t stream) {
+    using M = F32Geo<D, R, KT>;
+    static bool done[64] = {};
+    cudaError_t e = configure(differential_f32_kernel<D, R, KT>, M::SMEM, done);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmk, tmv;
+    std::memcpy(&tmk, tmap_k, sizeof tmk);
+    std::memcpy(&tmv, tmap_v, sizeof tmv);
+    const int grid = p.W < sms ? p.W : sms;
+    differential_f32_kernel<D, R, KT><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p, tmk, tmv);
+    return cudaGetLastError();
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-bool differential_needs_maps(int dtype, int D) { return use_mma(dtype, D); }
+bool differential_needs_maps(int dtype, int D) { return D == 64 || D == 128; }
+
+int differential_tile(int dtype, int D) { return tile_of(dtype, D); }
 
 int differential_rows(int dtype, int D, int G) {
     const int most = most_rows(dtype, D);
@@ -1416,7 +1856,12 @@ int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes,
     if (dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && D == DD && rows == RR) warps = CoreGeo<T, DD, RR>::WARPS;
     PKV_DF_CORE(PKV_DF_WARPS)
 #undef PKV_DF_WARPS
-    const int64_t tiles = lanes * ((max_len + kTile - 1) / kTile);
+#define PKV_DF_WARPS(DD, RR, KT) \
+    if (dtype == PKV_F32 && D == DD && rows == RR) warps = F32Geo<DD, RR, KT>::WARPS;
+    PKV_DF_F32(PKV_DF_WARPS)
+#undef PKV_DF_WARPS
+    const int tile = tile_of(dtype, D);
+    const int64_t tiles = lanes * ((max_len + tile - 1) / tile);
     int64_t w = (int64_t)warps * num_sms;
     if (w > kMaxWorkers) w = kMaxWorkers / num_sms * num_sms;
     if (tiles < w) w = tiles < 1 ? 1 : tiles;
@@ -1455,6 +1900,7 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
     p.R = a.rows;
     p.subs = a.ntok ? (a.block_tokens * a.G + a.rows - 1) / a.rows : (a.G + a.rows - 1) / a.rows;
     p.P = a.P;
+    p.tile = tile_of(a.dtype, a.D);
     p.window = a.window;
     p.qscale = (float)(1.4426950408889634 / std::sqrt((double)a.D));
     p.lambda = a.diff.lambda;
@@ -1479,6 +1925,11 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
     if (a.dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && a.D == DD && a.rows == RR)        \
         e = launch_core<T, DD, RR>(p, a.sms, stream);
     PKV_DF_CORE(PKV_DF_LAUNCH)
+#undef PKV_DF_LAUNCH
+#define PKV_DF_LAUNCH(DD, RR, KT)                                                             \
+    if (a.dtype == PKV_F32 && a.D == DD && a.rows == RR)                                      \
+        e = launch_f32<DD, RR, KT>(p, a.tmap_k, a.tmap_v, a.sms, stream);
+    PKV_DF_F32(PKV_DF_LAUNCH)
 #undef PKV_DF_LAUNCH
     if (e != cudaSuccess) return e;
     if (a.ev_after) cudaEventRecord(a.ev_after, stream);

@@ -307,9 +307,13 @@ struct DifferentialChunkLayout {
     size_t rows, lens, tok0, ntok, first, total;
 };
 
-// The decode kernel loads through tensor maps of the pool as [pages][H][D/64][P][64],
-// boxes of 2 heads x 16 positions, 128-byte swizzle (bf16, head width 64 or 128).
+// At head width 64 and 128 the decode kernels load through tensor maps of the pool as
+// [pages][H][row chunks of 128 bytes][P][128 bytes], boxes of 2 heads x one tile of
+// positions, 128-byte swizzle.
 bool differential_needs_maps(int dtype, int D);
+
+// Positions of a tile.
+int differential_tile(int dtype, int D);
 
 // Query rows that share one pass over a lane's keys, for G query pairs per KV pair.
 int differential_rows(int dtype, int D, int G);

@@ -90,7 +90,7 @@ struct pkv_pool {
     bool differential = false;         // requests carry the differential calls' scratch
     std::vector<CUtensorMap> tmap_k;   // per layer, when tmaps
     std::vector<CUtensorMap> tmap_v;
-    std::vector<CUtensorMap> pair_k;   // per layer, for the differential decode (bf16, 64 / 128)
+    std::vector<CUtensorMap> pair_k;   // per layer, for the differential decode (head_dim 64, 128)
     std::vector<CUtensorMap> pair_v;
     // failure injection (pkv_pool_inject_fault), each hook one-shot
     int64_t inject_lease = 0;          // > 0: page leases until the one that fails
@@ -253,20 +253,22 @@ bool encode_pool_map(CUtensorMap* map, void* base, int64_t rows, int D, int dtyp
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// One layer's K or V pool of bf16 heads as [pages][H][D/64][P][64], read in boxes of
-// one page's 16 positions x all of D x 2 heads with the 128-byte swizzle.
+// One layer's K or V pool as [pages][H][chunks][P][128 bytes of a row], read in boxes of
+// one tile of a page's positions x a whole row x 2 heads with the 128-byte swizzle.
 bool encode_pair_map(CUtensorMap* map, void* base, const pkv_pool* p) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
-    const cuuint64_t row = (cuuint64_t)p->head_dim * 2;
-    cuuint64_t dims[5] = {64, (cuuint64_t)p->page_size, (cuuint64_t)(p->head_dim / 64), (cuuint64_t)p->heads,
+    const int es = elem_bytes(p->dtype);
+    const cuuint64_t row = (cuuint64_t)p->head_dim * es, chunk = 128 / es;
+    cuuint64_t dims[5] = {chunk, (cuuint64_t)p->page_size, row / 128, (cuuint64_t)p->heads,
                           (cuuint64_t)p->pages};
     cuuint64_t strides[4] = {row, 128, row * p->page_size, row * p->page_size * p->heads};
-    cuuint32_t box[5] = {64, (cuuint32_t)pkv::kTile, (cuuint32_t)(p->head_dim / 64), 2, 1};
+    cuuint32_t box[5] = {(cuuint32_t)chunk, (cuuint32_t)pkv::differential_tile(p->dtype, p->head_dim),
+                         (cuuint32_t)(row / 128), 2, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, p->dtype == PKV_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              5, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ---- differential calls --------------------------------------------------------
@@ -276,23 +278,35 @@ int diff_rows(const pkv_pool* p) { return pkv::differential_rows(p->dtype, p->he
 // Row blocks per (request, KV pair) of a decode.
 int64_t diff_subs(const pkv_pool* p) { return (p->group + diff_rows(p) - 1) / diff_rows(p); }
 
-int diff_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
-    return pkv::differential_workers(p->dtype, p->head_dim, diff_rows(p), p->sms,
-                                     requests * (p->heads / 2) * diff_subs(p),
+// Workers of a launch over requests (or chunk blocks) of at most `rows` query rows a lane.
+int diff_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len, int rows, int64_t subs) {
+    return pkv::differential_workers(p->dtype, p->head_dim, rows, p->sms, requests * (p->heads / 2) * subs,
                                      pkv::attended_len(max_seq_len, p->window));
 }
 
-size_t diff_decode_bytes(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
-    return pkv::differential_layout(p->head_dim, diff_rows(p), diff_workers(p, requests, max_seq_len)).total;
+int diff_decode_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
+    return diff_workers(p, requests, max_seq_len, diff_rows(p), diff_subs(p));
 }
 
-// A prefill through lanes: blocks of bt chunk tokens are its requests.
+size_t diff_decode_bytes(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
+    return pkv::differential_layout(p->head_dim, diff_rows(p), diff_decode_workers(p, requests, max_seq_len))
+        .total;
+}
+
+// A prefill through lanes: blocks of bt chunk tokens are its requests, a block's tokens
+// rows of one lane.
 int diff_block_tokens(const pkv_pool* p) {
     return pkv::differential_block_tokens(p->dtype, p->head_dim, p->group);
 }
 
+int diff_chunk_rows(const pkv_pool* p) {
+    const int bt = diff_block_tokens(p);
+    return bt > 1 ? bt * p->group : diff_rows(p);
+}
+
 int diff_chunk_workers(const pkv_pool* p, int batch, int64_t n) {
-    return diff_workers(p, n / diff_block_tokens(p) + batch, p->max_context);
+    const int64_t rows = diff_chunk_rows(p), all = (int64_t)diff_block_tokens(p) * p->group;
+    return diff_workers(p, n / diff_block_tokens(p) + batch, p->max_context, (int)rows, (all + rows - 1) / rows);
 }
 
 // The tensor-core prefill serves the pool (it needs no scratch); else lanes.
@@ -302,7 +316,7 @@ bool diff_tensor_prefill(const pkv_pool* p) {
 
 size_t diff_prefill_bytes(const pkv_pool* p, int batch, int64_t n) {
     if (diff_tensor_prefill(p)) return 0;
-    return pkv::differential_chunk_layout(n, batch, diff_block_tokens(p), p->head_dim, diff_rows(p),
+    return pkv::differential_chunk_layout(n, batch, diff_block_tokens(p), p->head_dim, diff_chunk_rows(p),
                                           diff_chunk_workers(p, batch, n)).total;
 }
 
@@ -1364,6 +1378,7 @@ cudaError_t enqueue_diff_prefill(pkv_pool* p, int layer, pkv::DifferentialArgs& 
                                                 &p->tmap_v[(size_t)layer], s);
     a.q_bf16 = p->dtype == PKV_BF16;
     a.block_tokens = diff_block_tokens(p);
+    a.rows = diff_chunk_rows(p);
     a.workers = diff_chunk_workers(p, batch, total_new);
     return pkv::launch_differential_chunks(a, batch, total_new, cu_new, s);
 }
@@ -1492,7 +1507,7 @@ int pkv_paged_differential_decode(pkv_pool* p, int layer, int batch, const float
     a.max_seq_len = max_seq_len;
     a.out = out;
     a.workspace = workspace;
-    a.workers = diff_workers(p, batch, max_seq_len);
+    a.workers = diff_decode_workers(p, batch, max_seq_len);
     cudaError_t e = pkv::launch_differential(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
     return ok();
@@ -1583,7 +1598,7 @@ int pkv_append_and_attend_differential(pkv_request* r, int layer, const float* q
     a.max_seq_len = r->position + 1;
     a.out = out;
     a.workspace = r->dev_diff_ws;
-    a.workers = diff_workers(p, 1, r->position + 1);
+    a.workers = diff_decode_workers(p, 1, r->position + 1);
     cudaError_t e = pkv::launch_differential(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
     r->appended[(size_t)layer] = 1;
