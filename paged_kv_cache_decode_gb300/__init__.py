@@ -63,8 +63,13 @@ def _dtype_code(dtype) -> int:
     raise ValueError(f"unsupported storage dtype {dtype!r}")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

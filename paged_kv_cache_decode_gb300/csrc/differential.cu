@@ -81,6 +81,8 @@ struct DfParams {
     int normalise;
     float norm_eps, out_scale;
     float* out;                 // [token][Hp * G][2 D]
+    int alone;                  // > 0: one request, each lane split over this many warps of a
+                                //   CTA that join it in shared memory (no rec, no partials)
     int4* rec;                  // [W] lane that starts in worker w and ends after it:
                                 //   (request, pair * subs + sub, last worker, 1), or w = 0
     float2* part_ml;            // [2 W][R][2]
@@ -133,6 +135,11 @@ struct Prefix {
 
 __device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& entries) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    if (p.B == 1) {                             // nothing to scan
+        if (tid == 0 && blockIdx.x == 0 && !len_ok(p, len_at(p, 0))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+        stride = entries = 1;
+        return units_at(p, 0);
+    }
     const int nw = nt >> 5;
     stride = (p.B + kPrefix - 1) / kPrefix;
     entries = (p.B + stride - 1) / stride;
@@ -196,7 +203,7 @@ __device__ Cursor cursor_at(const DfParams& p, const Prefix& s, int stride, int 
         if (LN * s.pre[mid] <= f) lo = mid;
         else hi = mid - 1;
     }
-    int64_t base = LN * s.pre[lo];
+    int64_t base = p.B == 1 ? 0 : LN * s.pre[lo];
     Cursor c;
     c.x = lo * stride;
     for (;;) {
@@ -208,7 +215,7 @@ __device__ Cursor cursor_at(const DfParams& p, const Prefix& s, int stride, int 
     cursor_load(p, c);
     const int64_t local = f - base;
     const int per = c.n + kLaneCost;
-    c.ln = (int)(local / per);
+    c.ln = local < INT32_MAX ? (int)local / per : (int)(local / per);
     c.tile = (int)(local - (int64_t)c.ln * per) - kLaneCost;
     c.f = f;
     if (c.tile < 0) {
@@ -274,11 +281,25 @@ struct Share {
 __device__ __forceinline__ Share share_of(const DfParams& p, int64_t requests_units, int w) {
     Share s;
     s.all = (int64_t)p.Hp * p.subs * requests_units;
+    if (p.alone) {                              // warp w % alone of lane w / alone
+        const int n = requests_units > 0 ? (int)requests_units - kLaneCost : 0;
+        const int lane = w / p.alone, j = w - lane * p.alone;
+        const int64_t first = lane * requests_units + kLaneCost;
+        s.workers = p.W;
+        s.begin = first + j * n / p.alone;
+        s.end = first + (j + 1) * n / p.alone;
+        return s;
+    }
     s.workers = (int)(s.all < p.W ? s.all : p.W);
     s.begin = s.end = 0;
     if (w >= s.workers) return s;
-    s.begin = w * s.all / s.workers;
-    s.end = (w + 1) * s.all / s.workers;
+    if (s.all < (1 << 20)) {                    // 32-bit divisions while w * all fits
+        s.begin = (uint32_t)w * (uint32_t)s.all / (uint32_t)s.workers;
+        s.end = (uint32_t)(w + 1) * (uint32_t)s.all / (uint32_t)s.workers;
+    } else {
+        s.begin = w * s.all / s.workers;
+        s.end = (w + 1) * s.all / s.workers;
+    }
     return s;
 }
 
@@ -294,7 +315,8 @@ __device__ __forceinline__ void zero_empty(const DfParams& p, int D) {
     const int n = p.Hp * p.G * 2 * D;
     for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
         if (tiles_at(p, x) > 0) continue;
-        for (int i = threadIdx.x; i < n; i += blockDim.x) p.out[(int64_t)x * n + i] = 0.f;
+        const int threads = p.alone ? 32 * p.alone : blockDim.x;
+        for (int i = threadIdx.x; i < n; i += threads) p.out[(int64_t)x * n + i] = 0.f;
     }
 }
 
@@ -337,6 +359,11 @@ __device__ __forceinline__ bool row_at(const DfParams& p, const LaneRows& L, int
     return ok;
 }
 
+// Fetch a tensor map into the descriptor cache.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // A warp, a few tiles ahead: fetch into L1 the queries that the lane at `c` starts with, or
 // the new key and value rows that it ends with.
 template <int D, int ES>
@@ -353,11 +380,99 @@ __device__ __forceinline__ void prefetch_rows(const DfParams& p, const Cursor& c
                 fetch(static_cast<const char*>(p.q) + row * 2 * D * es + (i % per) * 128);
         }
     }
+    if (c.tile == c.n - 1) {
+        // what the epilogue reads
+        if (lane == 0) fetch(reinterpret_cast<const char*>(p.lambda + L.h * p.G));
+        if (p.norm_weight && lane < (2 * D * 4 + 127) / 128)
+            fetch(reinterpret_cast<const char*>(p.norm_weight) + lane * 128);
+    }
     if (p.k_new != nullptr && c.tile == c.n - 1) {
         constexpr int per = (2 * D * ES + 127) / 128;
         const int64_t at = ((int64_t)c.x * p.Hp + L.h) * 2 * D * ES;
         for (int i = lane; i < 2 * per; i += 32)
             fetch(static_cast<const char*>(i < per ? p.k_new : p.v_new) + at + (i % per) * 128);
+    }
+}
+
+// A warp's output row from the differences `d` (vector v of lane l: columns 4 (32 v + l) ..)
+// and the sum of their squares.
+template <int D>
+__device__ __forceinline__ void store_row(const DfParams& p, int64_t row, const float4* d, float sq) {
+    float c = p.out_scale;
+    if (p.normalise) c *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
+#pragma unroll
+    for (int v = 0; v < 2 * D / 128; ++v) {
+        const int col = (v * 32 + (threadIdx.x & 31)) * 4;
+        float4 nw = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (p.normalise && p.norm_weight) {
+            nw.x = __ldg(p.norm_weight + col), nw.y = __ldg(p.norm_weight + col + 1);
+            nw.z = __ldg(p.norm_weight + col + 2), nw.w = __ldg(p.norm_weight + col + 3);
+        }
+        *reinterpret_cast<float4*>(p.out + row * 2 * D + col) =
+            make_float4(d[v].x * c * nw.x, d[v].y * c * nw.y, d[v].z * c * nw.z, d[v].w * c * nw.w);
+    }
+}
+
+// One request whose lanes are each split over p.alone warps of one CTA: after the warps'
+// pieces, their partials are joined in shared memory.  A warp's partial lies in its own
+// part of the ring (its tiles are used up): (m, l) [R][2], then o [R][2][2 D].
+constexpr int kPartOffset = 128;
+
+template <int D, int R>
+__device__ __forceinline__ void join_alone(const DfParams& p, unsigned char* smem, int warp_bytes, int warp,
+                                           bool worked) {
+    const int lane = threadIdx.x & 31;
+    if (!worked && lane < 2 * R)
+        reinterpret_cast<float2*>(smem + warp * warp_bytes)[lane] = make_float2(-INFINITY, 0.f);
+    asm volatile("bar.sync 2, %0;" ::"r"(32 * p.alone) : "memory");
+    const int ln = blockIdx.x, h = ln / p.subs;
+    const LaneRows L = lane_rows(p, 0, h, ln - h * p.subs);
+    for (int r = warp; r < R; r += p.alone) {
+        int64_t row;
+        int head, st, en;
+        if (!row_at(p, L, r, row, head, st, en)) continue;
+        constexpr int NV = 2 * D / 128;             // vectors of 4 columns a lane
+        float4 o[2][NV];
+        float inv[2];
+#pragma unroll
+        for (int mm = 0; mm < 2; ++mm) {
+            const float2 ml = lane < p.alone ? reinterpret_cast<const float2*>(smem + lane * warp_bytes)[r * 2 + mm]
+                                             : make_float2(-INFINITY, 0.f);
+            float mx = ml.x;
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float wt = ml.y > 0.f ? exp2f(ml.x - mx) : 0.f;
+            float lt = wt * ml.y;
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+            inv[mm] = lt > 0.f ? 1.f / lt : 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) o[mm][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.alone; ++j) {
+                const float c = __shfl_sync(0xffffffffu, wt, j);
+                if (c == 0.f) continue;             // no partial, or one that weighs nothing
+                const float4* x = reinterpret_cast<const float4*>(smem + j * warp_bytes + kPartOffset) +
+                                  (r * 2 + mm) * (2 * D / 4) + lane;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const float4 y = x[v * 32];
+                    o[mm][v].x = fmaf(c, y.x, o[mm][v].x), o[mm][v].y = fmaf(c, y.y, o[mm][v].y);
+                    o[mm][v].z = fmaf(c, y.z, o[mm][v].z), o[mm][v].w = fmaf(c, y.w, o[mm][v].w);
+                }
+            }
+        }
+        inv[1] *= __ldg(p.lambda + head);
+        float4 d[NV];
+        float sq = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            d[v].x = o[0][v].x * inv[0] - o[1][v].x * inv[1], d[v].y = o[0][v].y * inv[0] - o[1][v].y * inv[1];
+            d[v].z = o[0][v].z * inv[0] - o[1][v].z * inv[1], d[v].w = o[0][v].w * inv[0] - o[1][v].w * inv[1];
+            sq += d[v].x * d[v].x + d[v].y * d[v].y + d[v].z * d[v].z + d[v].w * d[v].w;
+        }
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, x);
+        store_row<D>(p, row, d, sq);
     }
 }
 
@@ -433,16 +548,17 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
     __shared__ Prefix prefix;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp * gridDim.x + blockIdx.x;
-    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    constexpr int stages = M::STAGES;
+    unsigned char* ring = smem + warp * stages * M::STAGE_BYTES;
     unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
     float* pw = reinterpret_cast<float*>(after + warp * M::P_BYTES);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(after + M::WARPS * M::P_BYTES) + warp * M::STAGES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after + M::WARPS * M::P_BYTES) + warp * stages;
     int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * (M::P_BYTES + M::STAGES * 8)) +
-                          warp * M::STAGES;
-    if (lane == 0) {
-        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+                          warp * stages;
+    if (lane == 0 && w < p.W) {
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
-        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+        if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
     }
     int stride, entries;
     const int64_t total = build_prefix(p, prefix, stride, entries);
@@ -477,7 +593,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
         cursor_next(p, prod);
     };
     int ahead = 0;                                  // tiles staged and not yet used
-    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
+    for (; ahead < stages && prod.f < share.end; ++ahead) issue(ahead);
 
     const bool own = lane * F < D;                  // D < 32: the lanes past D idle
     const int feat = own ? lane * F : 0;
@@ -517,7 +633,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
             }
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            give_up(p, bars, M::STAGES, s, parity, ahead);
+            give_up(p, bars, stages, s, parity, ahead);
             return;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
@@ -634,7 +750,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
         __syncwarp();
         if (prod.f < share.end) issue(s);
         else --ahead;
-        if (++s == M::STAGES) {
+        if (++s == stages) {
             s = 0;
             parity ^= 1u;
         }
@@ -714,8 +830,9 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
 //   weights  one exponential a lane and row (map lane / 16), through shared memory
 //   values   a lane owns 4 or 8 of the 2 D columns for all rows and both maps: V is read
 //            once, weights as broadcasts; packed two-lane FMAs
-// KT = 8: the same ring holds twice the warps, and with several rows the kernel is bound
-// by their instruction latency (a tile of R = 4 rows is about 640 instructions).
+// KT = 8 at D = 128: the same ring holds twice the warps, and with several rows the kernel
+// is bound by their instruction latency (ragged chunks in lanes of 4 tokens: 124 us, with
+// KT = 16 139 us); at D = 64 both are alike (window of 1000, 2 rows: 35 us).
 template <int D, int R, int KT>
 struct F32Geo {
     static constexpr int CH = D / 32;                      // 128-byte chunks of a row
@@ -746,26 +863,32 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = warp * gridDim.x + blockIdx.x;
-    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    if (p.alone && warp >= p.alone) return;
+    const int w = p.alone ? blockIdx.x * p.alone + warp : warp * gridDim.x + blockIdx.x;
+    constexpr int stages = M::STAGES;
+    unsigned char* ring = smem + warp * stages * M::STAGE_BYTES;
     unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
     float* qs = reinterpret_cast<float*>(after + warp * M::Q_BYTES);            // [R][2][D], scaled
     float* pw = reinterpret_cast<float*>(after + M::WARPS * M::Q_BYTES + warp * M::P_BYTES);
     after += M::WARPS * (M::Q_BYTES + M::P_BYTES);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * M::STAGES;
-    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * M::STAGES;
-    if (lane == 0) {
-        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * stages;
+    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * stages;
+    if (lane == 0 && w < p.W) {
+        prefetch_map(&tmk);
+        prefetch_map(&tmv);
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
-        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+        if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
     }
     int stride, entries;
     const int64_t total = build_prefix(p, prefix, stride, entries);
     zero_empty(p, D);
     const Share share = share_of(p, total, w);
-    if (share.begin == share.end) return;
-    Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
-    if (cur.f >= share.end) return;
+    if (p.alone && total == 0) return;              // an empty slot
+    const bool worked = share.begin < share.end;
+    if (!worked && !p.alone) return;
+    Cursor cur = cursor_at(p, prefix, stride, entries, worked ? share.begin : 0);
+    if (!worked) cur.f = share.end;
     Cursor prod = cur;
     Pager pager;
     const uint64_t policy = l2_stream_policy();
@@ -788,7 +911,7 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
         cursor_next(p, prod);
     };
     int ahead = 0;                                  // tiles staged and not yet used
-    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
+    for (; ahead < stages && prod.f < share.end; ++ahead) issue(ahead);
 
     const int key = lane % KT, quarter = lane / KT, half = lane >> 4;
     // 16-byte piece u of key row `key` and head hd is at hd * HEAD + (u / 8) * KT * 128 +
@@ -838,8 +961,8 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
             __syncwarp();
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            give_up(p, bars, M::STAGES, s, parity, ahead);
-            return;
+            give_up(p, bars, stages, s, parity, ahead);
+            break;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
         const int k0 = (cur.tile0 + cur.tile) * KT;
@@ -977,14 +1100,16 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
         __syncwarp();
         if (prod.f < share.end) issue(s);
         else --ahead;
-        if (++s == M::STAGES) {
+        if (++s == stages) {
             s = 0;
             parity ^= 1u;
         }
 
         const bool has_end = cur.tile == cur.n - 1;
         if (has_end || cur.f + 1 >= share.end) {    // the piece ends
-            const int slot = 2 * w + (has_start ? 1 : 0);
+            const int64_t slot = 2 * w + (has_start ? 1 : 0);
+            float2* ml = p.alone ? reinterpret_cast<float2*>(ring) : p.part_ml + slot * R * 2;
+            float* po = p.alone ? reinterpret_cast<float*>(ring + kPartOffset) : p.part_o + slot * R * 4 * D;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 int64_t row;
@@ -1011,36 +1136,26 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
                     }
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                    float c = p.out_scale;
-                    if (p.normalise) c *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
-#pragma unroll
-                    for (int v = 0; v < M::NV; ++v) {
-                        const int col = (v * 32 + lane) * 4;
-                        float4 nw = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if (p.normalise && p.norm_weight) {
-                            nw.x = __ldg(p.norm_weight + col), nw.y = __ldg(p.norm_weight + col + 1);
-                            nw.z = __ldg(p.norm_weight + col + 2), nw.w = __ldg(p.norm_weight + col + 3);
-                        }
-                        *reinterpret_cast<float4*>(p.out + row * 2 * D + col) = make_float4(
-                            d[v].x * c * nw.x, d[v].y * c * nw.y, d[v].z * c * nw.z, d[v].w * c * nw.w);
-                    }
+                    store_row<D>(p, row, d, sq);
                 } else {
-                    const int64_t at = ((int64_t)slot * R + r) * 2;
-                    if (lane % 16 == 0) p.part_ml[at + half] = make_float2(m[r], lt);
+                    if (lane % 16 == 0) ml[r * 2 + half] = make_float2(m[r], lt);
 #pragma unroll
                     for (int mm = 0; mm < 2; ++mm)
 #pragma unroll
                         for (int v = 0; v < M::NV; ++v)
-                            *reinterpret_cast<float4*>(p.part_o + (at + mm) * 2 * D + (v * 32 + lane) * 4) =
+                            *reinterpret_cast<float4*>(po + (r * 2 + mm) * 2 * D + (v * 32 + lane) * 4) =
                                 make_float4(acc[r][mm][v][0].x, acc[r][mm][v][0].y, acc[r][mm][v][1].x,
                                             acc[r][mm][v][1].y);
                 }
             }
-            if (has_start && !has_end && lane == 0)
+            if (has_start && !has_end && lane == 0 && !p.alone)
                 p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, cur.f - cur.tile + cur.n), 1);
         }
         cursor_next(p, cur);
     }
+    // a lane of one tile, or of one warp, is finished already
+    if (p.alone > 1 && total > kLaneCost + 1)
+        join_alone<D, R>(p, smem, M::STAGES * M::STAGE_BYTES, warp, worked);
 }
 
 // ------------------------------------------------------ tensor-core engine --
@@ -1137,23 +1252,29 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = warp * gridDim.x + blockIdx.x;
-    unsigned char* ring = smem + warp * M::STAGES * M::STAGE_BYTES;
+    if (p.alone && warp >= p.alone) return;
+    const int w = p.alone ? blockIdx.x * p.alone + warp : warp * gridDim.x + blockIdx.x;
+    constexpr int stages = M::STAGES;
+    unsigned char* ring = smem + warp * stages * M::STAGE_BYTES;
     unsigned char* after = smem + M::WARPS * M::STAGES * M::STAGE_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * M::STAGES;
-    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * M::STAGES;
-    if (lane == 0) {
-        for (int s = 0; s < M::STAGES; ++s) mbar_init(&bars[s], 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after) + warp * stages;
+    int32_t* stage_page = reinterpret_cast<int32_t*>(after + M::WARPS * M::STAGES * 8) + warp * stages;
+    if (lane == 0 && w < p.W) {
+        prefetch_map(&tmk);
+        prefetch_map(&tmv);
+        for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
-        if (w < p.W) p.rec[w] = make_int4(0, 0, 0, 0);
+        if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
     }
     int stride, entries;
     const int64_t total = build_prefix(p, prefix, stride, entries);
     zero_empty(p, D);
     const Share share = share_of(p, total, w);
-    if (share.begin == share.end) return;
-    Cursor cur = cursor_at(p, prefix, stride, entries, share.begin);
-    if (cur.f >= share.end) return;
+    if (p.alone && total == 0) return;              // an empty slot
+    const bool worked = share.begin < share.end;
+    if (!worked && !p.alone) return;
+    Cursor cur = cursor_at(p, prefix, stride, entries, worked ? share.begin : 0);
+    if (!worked) cur.f = share.end;
     Cursor prod = cur;
     Pager pager;
     const uint64_t policy = l2_stream_policy();
@@ -1176,7 +1297,7 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
         cursor_next(p, prod);
     };
     int ahead = 0;                                  // tiles staged and not yet used
-    for (; ahead < M::STAGES && prod.f < share.end; ++ahead) issue(ahead);
+    for (; ahead < stages && prod.f < share.end; ++ahead) issue(ahead);
 
     const int g = lane >> 2, t = lane & 3;          // fragment row, column pair
     const int mj = lane >> 3, mr = lane & 7;        // ldmatrix: matrix and row of this address
@@ -1220,16 +1341,20 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                 for (int ks = 0; ks < M::KS; ++ks) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float a[3], b[3];
-                        split3(x[ks][i].x * scale, a);
-                        split3(x[ks][i].y * scale, b);
+                        // what is left after 0, 1, 2 parts; rounding it gives the next part
+                        const float a0 = x[ks][i].x * scale, b0 = x[ks][i].y * scale;
+                        const uint32_t h0 = pack(a0, b0);
+                        const float a1 = a0 - __uint_as_float(h0 << 16);
+                        const float b1 = b0 - __uint_as_float(h0 & 0xffff0000u);
+                        const uint32_t h1 = pack(a1, b1);
+                        const float a2 = a1 - __uint_as_float(h1 << 16);
+                        const float b2 = b1 - __uint_as_float(h1 & 0xffff0000u);
+                        const uint32_t h2 = pack(a2, b2);
 #pragma unroll
                         for (int u = 0; u < QB; ++u) {
                             // parts: R <= 2 g % 4, R = 4 (hi, mid) then (lo, 0), R = 8 part u
                             const int part = R <= 2 ? g & 3 : R == 4 ? 2 * u + (g & 1) : u;
-                            const float xa = part == 0 ? a[0] : part == 1 ? a[1] : part == 2 ? a[2] : 0.f;
-                            const float xb = part == 0 ? b[0] : part == 1 ? b[1] : part == 2 ? b[2] : 0.f;
-                            qb[mm][ks][u][i] = pack(xa, xb);
+                            qb[mm][ks][u][i] = part == 0 ? h0 : part == 1 ? h1 : part == 2 ? h2 : 0u;
                         }
                     }
                 }
@@ -1246,8 +1371,8 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                     o[u][nb][0] = o[u][nb][1] = o[u][nb][2] = o[u][nb][3] = 0.f;
         }
         if (!mbar_wait_bounded(&bars[s], parity, kWaitNs)) {
-            give_up(p, bars, M::STAGES, s, parity, ahead);
-            return;
+            give_up(p, bars, stages, s, parity, ahead);
+            break;
         }
         unsigned char* stage = ring + s * M::STAGE_BYTES;
         const int k0 = (cur.tile0 + cur.tile) * kTile;
@@ -1409,7 +1534,7 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
         __syncwarp();
         if (prod.f < share.end) issue(s);
         else --ahead;
-        if (++s == M::STAGES) {
+        if (++s == stages) {
             s = 0;
             parity ^= 1u;
         }
@@ -1486,13 +1611,14 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                     }
                 }
             } else {
-                const int slot = 2 * w + (has_start ? 1 : 0);
+                const int64_t slot = 2 * w + (has_start ? 1 : 0);
+                float2* ml = p.alone ? reinterpret_cast<float2*>(ring) : p.part_ml + slot * R * 2;
+                float* part = p.alone ? reinterpret_cast<float*>(ring + kPartOffset) : p.part_o + slot * R * 4 * D;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    const int r = combo_row(i), mm = combo_map(i);
-                    const int64_t at = ((int64_t)slot * R + r) * 2 + mm;
-                    if (g == 0 && (R > 1 || (t & 1) == 0)) p.part_ml[at] = make_float2(m[i], l[i]);
-                    float* po = p.part_o + at * 2 * D + g;
+                    const int at = combo_row(i) * 2 + combo_map(i);
+                    if (g == 0 && (R > 1 || (t & 1) == 0)) ml[at] = make_float2(m[i], l[i]);
+                    float* po = part + at * 2 * D + g;
 #pragma unroll
                     for (int nb = 0; nb < M::NB; ++nb) {
                         const float x = value(i, nb, 0), y = value(i, nb, 1);
@@ -1504,12 +1630,15 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
                         }
                     }
                 }
-                if (has_start && lane == 0)
+                if (has_start && lane == 0 && !p.alone)
                     p.rec[w] = make_int4(cur.x, cur.ln, last_worker(share, cur.f - cur.tile + cur.n), 1);
             }
         }
         cursor_next(p, cur);
     }
+    // a lane of one tile, or of one warp, is finished already
+    if (p.alone > 1 && total > kLaneCost + 1)
+        join_alone<D, R>(p, smem, M::STAGES * M::STAGE_BYTES, warp, worked);
 }
 
 // ------------------------------------------------------------------ merge --
@@ -1763,13 +1892,18 @@ int most_rows(int dtype, int D) { return use_mma(dtype, D) ? 8 : D == 64 || D ==
     F(__nv_bfloat16, 2, 1) F(__nv_bfloat16, 4, 1) F(__nv_bfloat16, 8, 1)                  \
     F(__nv_bfloat16, 16, 1) F(__nv_bfloat16, 32, 1) F(__nv_bfloat16, 256, 1)
 
+// CTAs of a launch: workers go to CTA after CTA; or one lane a CTA.
+int grid_of(const DfParams& p, int sms) {
+    return p.alone ? p.W / p.alone : p.W < sms ? p.W : sms;
+}
+
 template <typename T, int D, int R>
 cudaError_t launch_core(const DfParams& p, int sms, cudaStream_t stream) {
     using M = CoreGeo<T, D, R>;
     static bool done[64] = {};
     cudaError_t e = configure(differential_core_kernel<T, D, R>, M::SMEM, done);
     if (e != cudaSuccess) return e;
-    const int grid = p.W < sms ? p.W : sms;
+    const int grid = grid_of(p, sms);
     differential_core_kernel<T, D, R><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
@@ -1784,7 +1918,7 @@ cudaError_t launch_mma(const DfParams& p, const void* tmap_k, const void* tmap_v
     CUtensorMap tmk, tmv;
     std::memcpy(&tmk, tmap_k, sizeof tmk);
     std::memcpy(&tmv, tmap_v, sizeof tmv);
-    const int grid = p.W < sms ? p.W : sms;
+    const int grid = grid_of(p, sms);
     differential_mma_kernel<D, R><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p, tmk, tmv);
     return cudaGetLastError();
 }
@@ -1802,13 +1936,7 @@ cudaError_t launch_mma_rows(const DfParams& p, const void* tmap_k, const void* t
 }
 
 // fp32 at head width 64 and 128: f(D, R, KT).
-#ifndef PKV_DF_KT64
-#define PKV_DF_KT64 16
-#endif
-#ifndef PKV_DF_KT128
-#define PKV_DF_KT128 8
-#endif
-constexpr int kTileF32_64 = PKV_DF_KT64, kTileF32_128 = PKV_DF_KT128;
+constexpr int kTileF32_64 = 16, kTileF32_128 = 8;
 #define PKV_DF_F32(F)                                                                     \
     F(64, 1, kTileF32_64) F(64, 2, kTileF32_64) F(64, 4, kTileF32_64)                      \
     F(128, 1, kTileF32_128) F(128, 2, kTileF32_128) F(128, 4, kTileF32_128)
@@ -1827,10 +1955,17 @@ cudaError_t launch_f32(const DfParams& p, const void* tmap_k, const void* tmap_v
     CUtensorMap tmk, tmv;
     std::memcpy(&tmk, tmap_k, sizeof tmk);
     std::memcpy(&tmv, tmap_v, sizeof tmv);
-    const int grid = p.W < sms ? p.W : sms;
+    const int grid = grid_of(p, sms);
     differential_f32_kernel<D, R, KT><<<grid, M::WARPS * 32, M::SMEM, stream>>>(p, tmk, tmv);
     return cudaGetLastError();
 }
+
+// A single request of up to kAloneTiles tiles a warp gives each lane to the warps of one
+// CTA, which join it in shared memory: one launch, no scratch.  One token on the device,
+// against the split over the GPU and its merge: 12 heads of 64, fp32, 128 / 256 positions
+// 9.6 / 11.2 us against 10.5 / 11.6; 8 heads of 128, bf16, 128 / 256 positions 12.8 / 14.2
+// against 14.1 / 14.8; at 512 positions the split wins (12.7 against 15.0; 17.3, 17.5).
+constexpr int kAloneTiles = 4;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -1850,7 +1985,10 @@ int differential_block_tokens(int dtype, int D, int G) {
     return G <= most ? most / G : 1;
 }
 
-int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes, int64_t max_len) {
+namespace {
+
+// Warps of a CTA of the split kernel.
+int warps_of(int dtype, int D, int rows) {
     int warps = use_mma(dtype, D) ? (D == 64 ? MmaGeo<64>::WARPS : MmaGeo<128>::WARPS) : 0;
 #define PKV_DF_WARPS(T, DD, RR) \
     if (dtype == (sizeof(T) == 4 ? PKV_F32 : PKV_BF16) && D == DD && rows == RR) warps = CoreGeo<T, DD, RR>::WARPS;
@@ -1860,16 +1998,31 @@ int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes,
     if (dtype == PKV_F32 && D == DD && rows == RR) warps = F32Geo<DD, RR, KT>::WARPS;
     PKV_DF_F32(PKV_DF_WARPS)
 #undef PKV_DF_WARPS
-    const int tile = tile_of(dtype, D);
-    const int64_t tiles = lanes * ((max_len + tile - 1) / tile);
-    int64_t w = (int64_t)warps * num_sms;
-    if (w > kMaxWorkers) w = kMaxWorkers / num_sms * num_sms;
-    if (tiles < w) w = tiles < 1 ? 1 : tiles;
-    return (int)w;
+    return warps;
 }
 
-DifferentialLayout differential_layout(int D, int rows, int workers) {
+}  // namespace
+
+DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, int64_t requests, int64_t lanes,
+                                     int64_t max_len) {
+    const int warps = warps_of(dtype, D, rows), tile = tile_of(dtype, D);
+    const int64_t per = (max_len + tile - 1) / tile, tiles = lanes * per;
+    DifferentialSplit s{};
+    if (requests == 1 && (D == 64 || D == 128) && per <= (int64_t)kAloneTiles * warps && lanes <= num_sms) {
+        s.alone = per < warps ? (int)per : warps;
+        s.workers = (int)lanes * s.alone;
+        return s;
+    }
+    int64_t w = (int64_t)warps * num_sms;
+    if (w > kMaxWorkers) w = kMaxWorkers / num_sms * num_sms;
+    s.workers = (int)(tiles < w ? (tiles < 1 ? 1 : tiles) : w);
+    return s;
+}
+
+DifferentialLayout differential_layout(int D, int rows, DifferentialSplit split) {
     DifferentialLayout L{};
+    if (split.alone) return L;
+    const int workers = split.workers;
     L.rec = 0;
     L.part_ml = up256(L.rec + sizeof(int4) * (size_t)workers);
     L.part_o = up256(L.part_ml + sizeof(float2) * 2 * 2 * (size_t)workers * rows);
@@ -1909,9 +2062,10 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
     p.norm_eps = a.diff.norm_eps;
     p.out_scale = a.diff.out_scale;
     p.out = a.out;
-    p.W = a.workers;
+    p.W = a.split.workers;
     p.err = a.dev_error;
-    const DifferentialLayout L = differential_layout(a.D, a.rows, a.workers);
+    p.alone = a.split.alone;
+    const DifferentialLayout L = differential_layout(a.D, a.rows, a.split);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     p.rec = reinterpret_cast<int4*>(ws + L.rec);
     p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
@@ -1933,6 +2087,7 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
 #undef PKV_DF_LAUNCH
     if (e != cudaSuccess) return e;
     if (a.ev_after) cudaEventRecord(a.ev_after, stream);
+    if (p.alone) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.W, (unsigned)p.R);
     cfg.blockDim = dim3(kMergeThreads);
@@ -1946,10 +2101,10 @@ cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream) 
 }
 
 DifferentialChunkLayout differential_chunk_layout(int64_t N, int batch, int block_tokens, int D, int rows,
-                                                  int workers) {
+                                                  DifferentialSplit split) {
     DifferentialChunkLayout L{};
     L.blocks = N / block_tokens + batch;
-    size_t at = differential_layout(D, rows, workers).total;
+    size_t at = differential_layout(D, rows, split).total;
     auto take = [&](int64_t n) {
         const size_t o = at;
         at = up256(at + sizeof(int32_t) * (size_t)n);
@@ -2007,7 +2162,7 @@ cudaError_t launch_differential_chunks(const DifferentialArgs& args, int batch, 
                                        const int32_t* cu_new, cudaStream_t stream) {
     DifferentialArgs a = args;
     const DifferentialChunkLayout L =
-        differential_chunk_layout(total_new, batch, a.block_tokens, a.D, a.rows, a.workers);
+        differential_chunk_layout(total_new, batch, a.block_tokens, a.D, a.rows, a.split);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     ChunkParams c = chunk_params(a, batch, total_new, cu_new);
     c.X = L.blocks;

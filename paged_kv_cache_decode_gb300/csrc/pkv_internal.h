@@ -263,6 +263,12 @@ cudaError_t launch_shared_prefix_hook(const void* ctx, cudaStream_t stream);
 
 // ------------------------------------------------ differential attention --
 
+// How a launch splits its lanes: over `workers` warps of the GPU, joined by a merge kernel
+// through scratch; or (one short request, alone > 0) each over `alone` warps of one CTA.
+struct DifferentialSplit {
+    int workers, alone;
+};
+
 // One launch of the differential decode path for one layer.
 struct DifferentialArgs {
     int dtype, B, H, G, D, P;   // H: KV heads (an even number); G: query pairs per KV pair
@@ -289,7 +295,7 @@ struct DifferentialArgs {
     const void* tmap_k;         // the layer's 5-D CUtensorMaps (host memory) where
     const void* tmap_v;         //   differential_needs_maps
     int rows;                   // query rows of one lane (differential_rows)
-    int workers;                // differential_workers
+    DifferentialSplit split;
     int sms;
     unsigned* dev_error;
     cudaEvent_t ev_before;      // optional: recorded around the split kernel
@@ -321,12 +327,14 @@ int differential_rows(int dtype, int D, int G);
 // Chunk tokens of one lane of a prefill through lanes.
 int differential_block_tokens(int dtype, int D, int G);
 
-// Workers of one launch over `lanes` lanes of at most max_len attended positions.
-int differential_workers(int dtype, int D, int rows, int num_sms, int64_t lanes, int64_t max_len);
+// Workers of one launch over `lanes` lanes, of all requests, of at most max_len attended
+// positions.
+DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, int64_t requests, int64_t lanes,
+                                     int64_t max_len);
 
-DifferentialLayout differential_layout(int D, int rows, int workers);
+DifferentialLayout differential_layout(int D, int rows, DifferentialSplit split);
 DifferentialChunkLayout differential_chunk_layout(int64_t N, int batch, int block_tokens, int D, int rows,
-                                                  int workers);
+                                                  DifferentialSplit split);
 
 // Enqueue the split and merge kernels on `stream`.
 cudaError_t launch_differential(const DifferentialArgs& a, cudaStream_t stream);

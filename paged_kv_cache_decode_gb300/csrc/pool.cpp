@@ -278,18 +278,20 @@ int diff_rows(const pkv_pool* p) { return pkv::differential_rows(p->dtype, p->he
 // Row blocks per (request, KV pair) of a decode.
 int64_t diff_subs(const pkv_pool* p) { return (p->group + diff_rows(p) - 1) / diff_rows(p); }
 
-// Workers of a launch over requests (or chunk blocks) of at most `rows` query rows a lane.
-int diff_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len, int rows, int64_t subs) {
-    return pkv::differential_workers(p->dtype, p->head_dim, rows, p->sms, requests * (p->heads / 2) * subs,
-                                     pkv::attended_len(max_seq_len, p->window));
+// A launch over requests (or chunk blocks) of at most `rows` query rows a lane.
+pkv::DifferentialSplit diff_split(const pkv_pool* p, int64_t requests, int64_t max_seq_len, int rows,
+                                  int64_t subs) {
+    return pkv::differential_split(p->dtype, p->head_dim, rows, p->sms, requests,
+                                   requests * (p->heads / 2) * subs,
+                                   pkv::attended_len(max_seq_len, p->window));
 }
 
-int diff_decode_workers(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
-    return diff_workers(p, requests, max_seq_len, diff_rows(p), diff_subs(p));
+pkv::DifferentialSplit diff_decode_split(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
+    return diff_split(p, requests, max_seq_len, diff_rows(p), diff_subs(p));
 }
 
 size_t diff_decode_bytes(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
-    return pkv::differential_layout(p->head_dim, diff_rows(p), diff_decode_workers(p, requests, max_seq_len))
+    return pkv::differential_layout(p->head_dim, diff_rows(p), diff_decode_split(p, requests, max_seq_len))
         .total;
 }
 
@@ -304,9 +306,11 @@ int diff_chunk_rows(const pkv_pool* p) {
     return bt > 1 ? bt * p->group : diff_rows(p);
 }
 
-int diff_chunk_workers(const pkv_pool* p, int batch, int64_t n) {
+pkv::DifferentialSplit diff_chunk_split(const pkv_pool* p, int batch, int64_t n) {
     const int64_t rows = diff_chunk_rows(p), all = (int64_t)diff_block_tokens(p) * p->group;
-    return diff_workers(p, n / diff_block_tokens(p) + batch, p->max_context, (int)rows, (all + rows - 1) / rows);
+    // at least two "requests": blocks of chunk tokens are never a single request's decode
+    return diff_split(p, n / diff_block_tokens(p) + batch + 1, p->max_context, (int)rows,
+                      (all + rows - 1) / rows);
 }
 
 // The tensor-core prefill serves the pool (it needs no scratch); else lanes.
@@ -317,7 +321,7 @@ bool diff_tensor_prefill(const pkv_pool* p) {
 size_t diff_prefill_bytes(const pkv_pool* p, int batch, int64_t n) {
     if (diff_tensor_prefill(p)) return 0;
     return pkv::differential_chunk_layout(n, batch, diff_block_tokens(p), p->head_dim, diff_chunk_rows(p),
-                                          diff_chunk_workers(p, batch, n)).total;
+                                          diff_chunk_split(p, batch, n)).total;
 }
 
 int check_diff(const pkv_pool* p, const pkv_differential* d, const void* out) {
@@ -750,7 +754,7 @@ int pkv_request_create(pkv_pool* p, pkv_request** out) {
             e = cudaMalloc(&r->dev_prefill_ws, r->prefill_ws_bytes);
         if (p->differential) {
             r->diff_ws_bytes = diff_decode_bytes(p, 1, p->max_context);
-            if (e == cudaSuccess) e = cudaMalloc(&r->dev_diff_ws, r->diff_ws_bytes);
+            if (e == cudaSuccess && r->diff_ws_bytes) e = cudaMalloc(&r->dev_diff_ws, r->diff_ws_bytes);
         }
         if (e != cudaSuccess) {
             cudaFree(r->dev_table);
@@ -1379,7 +1383,7 @@ cudaError_t enqueue_diff_prefill(pkv_pool* p, int layer, pkv::DifferentialArgs& 
     a.q_bf16 = p->dtype == PKV_BF16;
     a.block_tokens = diff_block_tokens(p);
     a.rows = diff_chunk_rows(p);
-    a.workers = diff_chunk_workers(p, batch, total_new);
+    a.split = diff_chunk_split(p, batch, total_new);
     return pkv::launch_differential_chunks(a, batch, total_new, cu_new, s);
 }
 
@@ -1482,7 +1486,7 @@ int pkv_paged_differential_decode(pkv_pool* p, int layer, int batch, const float
     if (batch < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "negative batch");
     if (int rc = check_diff(p, diff, out); rc != PKV_OK) return rc;
     if (batch > 0) {
-        if (!q || !k_new || !v_new || !page_tables || !seq_lens || !out || !workspace)
+        if (!q || !k_new || !v_new || !page_tables || !seq_lens || !out)
             return fail(PKV_ERR_INVALID_ARGUMENT, "NULL pointer");
         if (max_pages < 1 || max_seq_len < 1)
             return fail(PKV_ERR_INVALID_ARGUMENT, "max_pages and max_seq_len must be >= 1");
@@ -1493,6 +1497,7 @@ int pkv_paged_differential_decode(pkv_pool* p, int layer, int batch, const float
     if (p->host_only) return fail(PKV_ERR_NO_STORAGE, "host-only pool has no device storage");
     if (batch == 0) return ok();
     const size_t need = diff_decode_bytes(p, batch, max_seq_len);
+    if (need && !workspace) return fail(PKV_ERR_INVALID_ARGUMENT, "NULL workspace");
     if (workspace_bytes < need)
         return fail(PKV_ERR_INVALID_ARGUMENT, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if (int rc = check_device(p); rc != PKV_OK) return rc;
@@ -1507,7 +1512,7 @@ int pkv_paged_differential_decode(pkv_pool* p, int layer, int batch, const float
     a.max_seq_len = max_seq_len;
     a.out = out;
     a.workspace = workspace;
-    a.workers = diff_decode_workers(p, batch, max_seq_len);
+    a.split = diff_decode_split(p, batch, max_seq_len);
     cudaError_t e = pkv::launch_differential(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
     return ok();
@@ -1598,7 +1603,7 @@ int pkv_append_and_attend_differential(pkv_request* r, int layer, const float* q
     a.max_seq_len = r->position + 1;
     a.out = out;
     a.workspace = r->dev_diff_ws;
-    a.workers = diff_decode_workers(p, 1, r->position + 1);
+    a.split = diff_decode_split(p, 1, r->position + 1);
     cudaError_t e = pkv::launch_differential(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
     r->appended[(size_t)layer] = 1;

@@ -384,7 +384,7 @@ def test_prefill_device_refusals():
 
 
 def test_host_refusals():
-    c = Case([30], 2, 1, 64, dtype="bf16")
+    c = Case([30, 300], 2, 1, 64, dtype="bf16")        # two requests: scratch is needed
     plain = pkv.Pool(1, 4, 2, 64, 16, "bf16", 64)
     try:
         args = (0, c.q, c.k_new, c.v_new, c.tables, c.dlens, c.max_len)
