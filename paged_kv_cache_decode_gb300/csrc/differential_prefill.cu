@@ -1,42 +1,48 @@
 // Differential attention of prefill chunks on the sm_103a tensor cores (bf16 pools of
 // head width 64 or 128); differential.cu holds the formula and every other pool.
 //
-// Two launches per call: the chunk's rows are stored in their pages, then one CTA
-// per (query tile, KV pair, output half) attends them.
+// Two launches per call: the chunk's rows are stored in their pages, then one cluster
+// of two CTAs per (query tile, KV pair) attends them, one softmax map a CTA.
 //
 // Attention CTA.  A query tile is 128 rows: 128/G consecutive chunk tokens times the
-// G query pairs that share one KV pair.  Map 0 and map 1 of the same rows are two
-// score tiles, A and B, against the keys of the pair's first and second head; both
-// multiply the same values:
-//     S_A = Q_0 K_0^T, S_B = Q_1 K_1^T   tcgen05.mma, M=128 N=128 K=d_h, fp32 in TMEM
-//     P_x = 2^(c S_x - c m_x)            softmax warps: TMEM -> registers -> bf16 hi + lo
-//                                        back into TMEM over the S columns already read
-//     O_x += P_hi,x V + P_lo,x V         tcgen05.mma, A = P from TMEM, M=128 N=128 K=128
-// with c = log2(e) / sqrt(d_h).  S_A, S_B, O_A and O_B of 128 columns each fill the
-// 512 columns of TMEM, so one CTA holds 128 of the pair's 2 d_h value columns: both
-// heads' at d_h = 64; at d_h = 128 the two CTAs of a cluster take one head's each
-// and compute the scores twice (12 units of MMA work per key tile where one CTA per
-// map would need 10, but the same code for both widths and no exchange of O).
-// Warp roles (320 threads):
-//   warps 0-3, 4-7  softmax of A, B: one query row per thread; they stage Q, write P,
-//              rescale O.  At the end each group takes 64 output columns of the
-//              same rows: d = O_A / l_A - lambda O_B / l_B, mean square over all
-//              2 d_h columns (across the cluster through distributed shared
-//              memory), store;
-//   warp 8     producer: eight lanes issue the K / V tile copies, one 16-row group
-//              each (a group never straddles a page);
-//   warp 9     MMA: allocates TMEM, one thread issues the MMAs and commits.
-// The MMA order P V_A(j), S_A(j+1), P V_B(j), S_B(j+1) ... keeps the tensor cores on
-// one map while the other map's softmax runs; MMAs of one thread run in issue order,
-// so S_A(j+1) overwrites P_A(j) only after P V_A(j) has read it.
+// G query pairs that share one KV pair.  The CTA of map m takes the pair's queries
+// q_(2i+m) against the keys of head 2p + m, and the values of both heads:
+//     S  = Q_m K_m^T           tcgen05.mma, M=128 N=128 K=d_h, fp32 in TMEM
+//     P  = 2^(c S - c base)    softmax warps: TMEM -> registers -> bf16 hi + lo
+//                              back into TMEM over the S columns already read
+//     O += P_hi V + P_lo V     tcgen05.mma, A = P from TMEM, M=128 N=2 d_h K=128
+// with c = log2(e) / sqrt(d_h).  S has BUFS buffers of 128 columns beside O's 2 d_h, and
+// a group of four softmax warps each: S of the next tiles is there before a tile's
+// softmax ends, and the groups' softmaxes overlap -- the softmax of one tile (TMEM round
+// trips, exponentials) takes longer than its MMAs, so with one S a map the tensor
+// cores were 43 % busy.  MMA order P V(j), S(j + BUFS): MMAs of one thread run in issue
+// order, so S overwrites P(j) only after P V(j) has read it.
+//
+// The groups share one exponent base per row, handed from tile to tile through shared
+// memory as soon as a tile's maximum is known.  It moves only when the maximum grows by
+// more than 8 in log2 units (weights stay below 2^8; O / l uses the same base in both);
+// the group that moves it waits for the previous P V and rescales O.
+//
+// At the end CTA m scales its O by 1 / l (map 1: lambda / l), sends the other CTA the
+// d_h columns that that one finishes through distributed shared memory, and both take
+// d = map 0 - map 1, its mean square over all 2 d_h columns, and store their half.
+//
+// Warp roles (256 BUFS + 96 threads): softmax groups (two threads per query row; they
+// stage Q, write P, rescale O, store the output); two producers, for K and for V (copies of
+// 16-row groups: a group never straddles a page); an MMA warp (allocates TMEM, one
+// thread issues the MMAs and commits).  MMAs and copies are issued under elect.sync: in
+// a branch on the lane number every operand is moved to uniform registers each time, at
+// about 100 cycles an instruction, and that bounded the kernel (4 x 2048 tokens, d_h =
+// 128: 414 us against XXX).
 //
 // Bound: the tensor cores (P V twice for the hi and lo parts of the weights, which
-// carry each to about 2^-17; one bf16 part alone would be off by 2^-9).  The row
-// maximum is only followed when it grows by more than 8 in log2 units (the weights
-// stay below 2^8 and O / l uses the same base in both).
+// carry each to about 2^-17; one bf16 part alone would be off by 2^-9).  O accumulates
+// inside the tensor cores, whose additions truncate: 5e-6 off the formula at 4096
+// positions, 2e-5 at 16384.
 //
 // Faults: bad lengths and page ids set bits of the device error word (a bad page
-// reads as zeros); a wait that runs out sets the timeout bit and ends the CTA's work.
+// reads as zeros); a wait that runs out sets the timeout bit and ends the CTA's work
+// (it still meets the other CTA at the cluster barriers).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -57,29 +63,89 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows per tile = TMEM lanes
 constexpr int kKeys = 128;                  // key positions per key tile
-constexpr int kCols = 128;                  // value columns of one CTA
-constexpr int kThreads = 320;
+
+// Bounded wait of a whole warp; gives up early once another role of the CTA has given up.
+__device__ __forceinline__ bool dp_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned* dev_error) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t start = global_timer_ns();
+        for (uint32_t i = 1; !ok; ++i) {
+            ok = mbar_try_wait(bar, parity);
+            if (!ok && (i & 63) == 0) {
+                if (*abort_flag) break;
+                if (global_timer_ns() - start > kTcWaitLimitNs) {
+                    *abort_flag = 1;
+                    atomicOr(dev_error, PKV_DEVERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// 16 or 32 consecutive 32-bit columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+    if constexpr (N == 32) {
+        tmem_ld32(taddr, r);
+    } else {
+        static_assert(N == 16, "16 or 32 columns");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+              "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+    }
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(x));
+    return x != 0;
+}
 
 template <int D>
 struct DpGeo {
-    static constexpr int HALVES = 2 * D / kCols;             // CTAs (a cluster) per pair and tile
+    static constexpr int BUFS = 2;                           // S buffers = softmax groups
+    static constexpr int SOFTMAX = 256 * BUFS;               // softmax threads
+    static constexpr int THREADS = SOFTMAX + 96;             // and two producer warps, the MMA warp
     static constexpr int CHUNKS = D / 64;                    // 128-byte swizzle columns of Q, K
     static constexpr int COL_BYTES = kKeys * 128;            // one such column of 128 rows
-    static constexpr int Q_BYTES = CHUNKS * COL_BYTES;       // Q of one map
-    static constexpr int SLOT = 2 * COL_BYTES;               // 128 keys x 128 columns
-    // loads of one key tile, one slot each: D = 64 the pair's K, its V; D = 128 K of map 0,
-    // K of map 1, V of this CTA's head
-    static constexpr int LOADS = D == 64 ? 2 : 3;
+    static constexpr int Q_BYTES = CHUNKS * COL_BYTES;       // Q, or the K of a tile
+    static constexpr int V_BYTES = 2 * Q_BYTES;              // both heads' V of a tile
+    static constexpr int V_GROUP = V_BYTES / 8;              // 16 positions of it
+    static constexpr int STAGE = Q_BYTES + V_BYTES;
     static constexpr int BAR_BYTES = 256;
-    static constexpr int XCH_BYTES = HALVES > 1 ? 2 * kRows * 4 : 0;   // sums from the other CTA
-    static constexpr int FIXED = 1024 + 2 * Q_BYTES + BAR_BYTES + XCH_BYTES;
-    static constexpr int SLOTS_FIT = (227 * 1024 - FIXED) / SLOT;
-    static constexpr int SLOTS = SLOTS_FIT < 6 ? SLOTS_FIT : 6;
-    static constexpr int SMEM = FIXED + SLOTS * SLOT;
-    static constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
+    // the rows' exponent bases (this tile's and the last one's), and either key half's
+    // maximum for each group, all bf16
+    static constexpr int ROW_BYTES = (2 + 2 * BUFS) * kRows * 2;
+    static constexpr int FIXED = 1024 + Q_BYTES + BAR_BYTES + ROW_BYTES;
+    static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE < 4 ? (227 * 1024 - FIXED) / STAGE : 4;
+    static constexpr int SMEM = FIXED + STAGES * STAGE;
+    static constexpr uint32_t O_COL = 512 - 2 * D, TMEM_COLS = 512;
     static_assert(D == 64 || D == 128, "head width 64 or 128");
-    static_assert(SLOTS >= LOADS + 1 && SMEM <= 227 * 1024, "CTA does not fit an SM");
-    static_assert(2 * SLOTS * 8 + 8 * 8 + 16 <= BAR_BYTES, "barrier area");
+    static_assert(BUFS * kKeys <= (int)O_COL, "S buffers and O fill TMEM");
+    static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "CTA does not fit an SM");
+    static_assert((4 * STAGES + 3 * BUFS + 3) * 8 + 16 <= BAR_BYTES, "barrier area");
+    static_assert(STAGES * STAGE >= kRows * D * 4, "the other CTA's columns go over the ring");
 };
 
 struct DpParams {
@@ -142,33 +208,39 @@ __device__ int2 find_tile(const DpParams& p, int item, bool report) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(DpGeo<D>::THREADS, 1)
 differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv) {
     using M = DpGeo<D>;
-    constexpr int HV = M::HALVES;
+    constexpr int NB = M::BUFS, NS = M::STAGES;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* Qs = sm;                                   // maps A, B
-    unsigned char* ring = Qs + 2 * M::Q_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + M::SLOTS * M::SLOT);
-    uint64_t* slot_full = bars;                  // per slot: copy landed
-    uint64_t* slot_empty = bars + M::SLOTS;      //           MMAs reading it done
-    uint64_t* s_full = bars + 2 * M::SLOTS;      // per map: S computed
-    uint64_t* p_full = s_full + 2;               //          P written
-    uint64_t* o_done = p_full + 2;               // last P V of both maps done
+    unsigned char* Qs = sm;
+    unsigned char* ring = Qs + M::Q_BYTES;       // per stage: K, then V of both heads
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * M::STAGE);
+    uint64_t* k_full = bars;                     // per stage: K landed
+    uint64_t* v_full = bars + NS;                //            V landed
+    uint64_t* k_empty = bars + 2 * NS;           //            S that reads the K done
+    uint64_t* v_empty = bars + 3 * NS;           //            P V that reads the V done
+    uint64_t* s_full = bars + 4 * NS;            // per buffer: S computed
+    uint64_t* p_full = s_full + NB;              //             P written
+    uint64_t* pv_done = p_full + NB;             //             P V of the buffer's tile done
+    uint64_t* o_done = pv_done + NB;             // the last P V done
     uint64_t* q_ready = o_done + 1;
     uint64_t* drain = q_ready + 1;               // MMA completion on the abort path
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tile_s = const_cast<int*>(abort_flag) + 1;           // request, tile
-    float* peer_sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(bars) + M::BAR_BYTES);
+    __nv_bfloat16* base_s =
+        reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(bars) + M::BAR_BYTES);   // [2][128]
+    __nv_bfloat16* row_max = base_s + 2 * kRows;                                     // [group][half][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // CTAs: item-major, then KV pair, then (cluster) half
-    const int half = HV == 2 ? (int)(blockIdx.x & 1) : 0;
-    const int unit = blockIdx.x / HV;
+    constexpr int kProducer = M::SOFTMAX / 32, kMma = kProducer + 2;
+    // CTAs: item-major, then KV pair, then map (a cluster's two CTAs)
+    const int map = blockIdx.x & 1;
+    const int unit = blockIdx.x >> 1;
     const int item = unit / p.Hp, h = unit - item * p.Hp;
     if (warp == 0) {
         if (blockIdx.x == 0) find_tile(p, 0, true);
@@ -180,26 +252,23 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         }
     }
     if (threadIdx.x == 32) {
-        for (int s = 0; s < M::SLOTS; ++s) {
-            mbar_init(&slot_full[s], 1);
-            mbar_init(&slot_empty[s], 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128);
+        for (int s = 0; s < 4 * NS; ++s) mbar_init(&bars[s], 1);
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_full[b], 256);
+            mbar_init(&pv_done[b], 1);
         }
         mbar_init(o_done, 1);
-        mbar_init(q_ready, 256);
+        mbar_init(q_ready, M::SOFTMAX);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
     __syncthreads();
     const int b = tile_s[0];
     if (b < 0) return;                           // both CTAs of a cluster alike
-    if (warp == 9) tmem_alloc(tmem_slot, M::TMEM_COLS);
+    if (warp == kMma) tmem_alloc(tmem_slot, M::TMEM_COLS);
     tc_fence_before();
-    if constexpr (HV == 2) cluster_sync_all();   // the other CTA runs: its shared memory may be written
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -211,24 +280,24 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     const int lo_first = p.window > 0 && L0 + i0 + 1 > p.window ? (int)(L0 + i0 + 1 - p.window) : 0;
     const int kt0 = lo_first / kKeys, ntiles = pos_last / kKeys - kt0 + 1;
 
-    // rows of the output and what the epilogue needs of them
-    const int r = threadIdx.x & 127;                          // softmax warps: row = TMEM lane
-    const int g = r % G, i = i0 + r / G;
-    const bool valid = i < i_end;
-    const int heads = p.Hp * G, head = h * G + g;
-    const int64_t row_x = (int64_t)c0 + i;
-
-    if (warp < 8) {
+    if (warp < kProducer) {
         // ------------------------------------------------------ softmax --
-        const int x = warp >> 2;                              // map A (0) or B (1)
-        unsigned char* Qx = Qs + x * M::Q_BYTES;
+        const int grp = warp >> 3;                            // takes tiles grp, grp + NB, ...
+        const int kh = (warp >> 2) & 1;                       // keys 64 kh .. 64 kh + 63 of them
+        const int r = threadIdx.x & 127;                      // row of the tile = TMEM lane
+        const int g = r % G, i = i0 + r / G;
+        const bool valid = i < i_end;
+        const int heads = p.Hp * G, head = h * G + g;
+        const int64_t row_x = (int64_t)c0 + i;
+        const int part = grp * 2 + kh;
         {
             const uint4* src =
-                reinterpret_cast<const uint4*>(p.q + ((row_x * heads + head) * 2 + x) * D);
+                reinterpret_cast<const uint4*>(p.q + ((row_x * heads + head) * 2 + map) * D);
 #pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-                const uint4 v = valid ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(Qx + sw_off(r, u)) = v;
+            for (int u = 0; u < D / 8 / (2 * NB); ++u) {
+                const int piece = part * (D / 8 / (2 * NB)) + u;
+                const uint4 v = valid ? __ldg(src + piece) : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(Qs + sw_off(r, piece)) = v;
             }
         }
         fence_proxy_async_smem();
@@ -239,296 +308,326 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         const int lo = p.window > 0 && pos + 1 > p.window ? (int)(pos + 1 - p.window) : 0;
         const float c = p.scale_log2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = lanes + M::S_COL + x * kKeys;
-        const uint32_t t_o = lanes + M::O_COL + x * kCols;
+        const uint32_t t_s = lanes + grp * kKeys + kh * 64;
+        const uint32_t t_o = lanes + M::O_COL;
+        // A named barrier for each group and row quarter: the two warps of tile j meet, and
+        // the two of tile j - 1 have arrived with its base (before tile 0: the last group).
+        const int bar_in = 1 + grp * 4 + (warp & 3), bar_out = 1 + (grp + 1) % NB * 4 + (warp & 3);
+        __nv_bfloat16* mine = row_max + part * kRows + r;
+        const __nv_bfloat16* other = row_max + (part ^ 1) * kRows + r;
+        if (grp == NB - 1) {
+            if (kh == 0) base_s[kRows + r] = __float2bfloat16_rn(-INFINITY);
+            asm volatile("bar.arrive %0, 128;" ::"r"(bar_out) : "memory");
+        }
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < ntiles; ++j) {
-            if (!pf_warp_wait(&s_full[x], j & 1, abort_flag, p.dev_error)) {
-                ok = false;
-                break;
-            }
+        for (int j = grp; j < ntiles; j += NB) {
+            if (!dp_warp_wait(&s_full[grp], (j / NB) & 1, abort_flag, p.dev_error)) ok = false;
             tc_fence_after();
-            // keys e_lo .. e_hi of the tile are this row's (none when e_lo > e_hi)
-            const int k0 = (kt0 + j) * kKeys;
-            const bool full = k0 >= lo && k0 + kKeys - 1 <= hi;
-            const int e_lo = min(max(lo - k0, 0), kKeys), e_hi = max(min(hi - k0, kKeys - 1), -1);
-            // the row maximum first (keys 64..127 read for it alone), then the weights of keys
-            // 0..63 from registers and of 64..127 from a second read; P_hi and P_lo of a half
-            // go over that half's S columns: 32 columns of pairs each
-            const float2 c2 = make_float2(c, c);
-            float m2[2] = {-INFINITY, -INFINITY};
-            auto mask = [&](uint32_t* s, int first) {
-                if (full) return;
+            // keys e_lo .. e_hi of this half are this row's (none when e_lo > e_hi)
+            const int k0 = (kt0 + j) * kKeys + kh * 64;
+            const bool full = k0 >= lo && k0 + 63 <= hi;
+            const int e_lo = max(lo - k0, 0), e_hi = min(hi - k0, 63);
+            auto load = [&](uint32_t* sv, int chunk) {
+                tmem_ld32(t_s + chunk * 32, sv);
+                tmem_wait_ld();
+                if (!full) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (first + e < e_lo || first + e > e_hi) s[e] = 0xff800000u;
-            };
-            auto largest = [&](const uint32_t* s) {
-#pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    m2[0] = fmax3(m2[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                    m2[1] = fmax3(m2[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                    for (int e = 0; e < 32; ++e)
+                        if (chunk * 32 + e < e_lo || chunk * 32 + e > e_hi) sv[e] = 0xff800000u;
                 }
             };
-            {
-                uint32_t sv[64];
-                tmem_ld32(t_s + 64, sv);
-                tmem_ld32(t_s + 96, sv + 32);
-                tmem_wait_ld();
-                mask(sv, 64);
-                largest(sv);
+            // S is read twice, 32 columns at a time: for the maximum, then for the weights
+            float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int chunk = 0; chunk < 2; ++chunk) {
+                uint32_t sv[32];
+                load(sv, chunk);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    m2[0] = fmax3(m2[0], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                    m2[1] = fmax3(m2[1], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
+                }
             }
-            uint32_t s0[64];
-            tmem_ld32(t_s, s0);
-            tmem_ld32(t_s + 32, s0 + 32);
-            tmem_wait_ld();
-            mask(s0, 0);
-            largest(s0);
-            const float mx = fmaxf(m2[0], m2[1]);
-            float alpha = 1.f;
-            if (mx > m_used && (m_used == -INFINITY || (mx - m_used) * c > 8.f)) {
-                alpha = m_used == -INFINITY ? 0.f : ex2((m_used - mx) * c);
-                m_used = mx;
-                l *= alpha;
-            }
-            // S of this tile was committed after P V of the previous one, so that P V is
-            // complete: O may be rescaled
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // Maxima and bases are bf16: any base near the maximum serves, as long as all warps
+            // of a row take the same.  (The other warp has read `mine` of this group's last
+            // tile before it arrived on p_full, without which this S would not be there.)
+            const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(m2[0], m2[1]));
+            *mine = own;
+            asm volatile("bar.sync %0, 128;" ::"r"(bar_in) : "memory");
+            const float mx = fmaxf(__bfloat162float(own), __bfloat162float(*other));
+            const float before = __bfloat162float(base_s[((j + 1) & 1) * kRows + r]);    // of tile j - 1
+            const float base =
+                mx > before && (before == -INFINITY || (mx - before) * c > 8.f) ? mx : before;
+            if (kh == 0) base_s[(j & 1) * kRows + r] = __float2bfloat16_rn(base);
+            if (j + 1 < ntiles) asm volatile("bar.arrive %0, 128;" ::"r"(bar_out) : "memory");
+            // l is this thread's share, at the base of its last tile
+            if (base != m_used) l *= m_used == -INFINITY ? 0.f : ex2((m_used - base) * c);
+            m_used = base;
+            if (j > 0 && __any_sync(0xffffffffu, base != before)) {
+                // O was summed at the old base; it is whole once P V of tile j - 1 is done
+                const float alpha = base == before ? 1.f : before == -INFINITY ? 0.f : ex2((before - base) * c);
+                if (!dp_warp_wait(&pv_done[(j - 1) % NB], ((j - 1) / NB) & 1, abort_flag, p.dev_error))
+                    ok = false;
+                tc_fence_after();
 #pragma unroll 1
-                for (int cc = 0; cc < kCols / 32; ++cc) {
+                for (int cc = 0; cc < D / 32; ++cc) {         // half of O's columns a warp
                     uint32_t ov[32];
-                    tmem_ld32(t_o + cc * 32, ov);
+                    tmem_ld32(t_o + kh * D + cc * 32, ov);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                    tmem_st32(t_o + cc * 32, ov);
+                    tmem_st32(t_o + kh * D + cc * 32, ov);
                 }
                 tmem_wait_st();
             }
-            const float mb = m_used == -INFINITY ? 0.f : m_used * c;
-            const float2 nmb2 = make_float2(-mb, -mb);
+            const float mb = base == -INFINITY ? 0.f : base * c;
+            const float2 c2 = make_float2(c, c), nmb2 = make_float2(-mb, -mb), minus = make_float2(-1.f, -1.f);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto weights = [&](const uint32_t* sv, uint32_t col) {
-                uint32_t phi[32], plo[32];
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const float2 xe = __ffma2_rn(
-                        make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nmb2);
-                    const float2 pr = make_float2(ex2(xe.x), ex2(xe.y));
-                    acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], pr);
-                    const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
-                    const __nv_bfloat162 lb =
-                        __floats2bfloat162_rn(pr.x - __low2float(hb), pr.y - __high2float(hb));
-                    phi[e >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
-                    plo[e >> 1] = *reinterpret_cast<const uint32_t*>(&lb);
+            for (int chunk = 0; chunk < 2; ++chunk) {
+                uint32_t sv[32];
+                load(sv, chunk);
+#pragma unroll
+                for (int k = 0; k < 32; k += 16) {
+                    uint32_t pv[16];                          // 8 P_hi pairs, 8 P_lo pairs
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 xe = __ffma2_rn(
+                            make_float2(__uint_as_float(sv[k + e]), __uint_as_float(sv[k + e + 1])), c2, nmb2);
+                        const float2 pr = make_float2(ex2(xe.x), ex2(xe.y));
+                        acc[(e >> 1) & 1] = __fadd2_rn(acc[(e >> 1) & 1], pr);
+                        const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
+                        const float2 rest = __ffma2_rn(__bfloat1622float2(hb), minus, pr);   // exact
+                        const __nv_bfloat162 lb = __floats2bfloat162_rn(rest.x, rest.y);
+                        pv[e >> 1] = *reinterpret_cast<const uint32_t*>(&hb);
+                        pv[8 + (e >> 1)] = *reinterpret_cast<const uint32_t*>(&lb);
+                    }
+                    tmem_st16(t_s + chunk * 32 + k, pv);
                 }
-                tmem_st32(t_s + col, phi);
-                tmem_st32(t_s + col + 32, plo);
-            };
-            weights(s0, 0);
-            {
-                uint32_t sv[64];
-                tmem_ld32(t_s + 64, sv);
-                tmem_ld32(t_s + 96, sv + 32);
-                tmem_wait_ld();
-                mask(sv, 64);
-                weights(sv, 64);
             }
             tmem_wait_st();
             const float2 a = __fadd2_rn(acc[0], acc[1]);
             l += a.x + a.y;
             tc_fence_before();
-            mbar_arrive(&p_full[x]);
+            mbar_arrive(&p_full[grp]);
         }
-        if (ok) ok = pf_warp_wait(o_done, 0, abort_flag, p.dev_error);
-        // Q is no longer read: its first bytes carry 1 / l and the partial sums of squares
-        float* linv = reinterpret_cast<float*>(Qs);           // [2][128]
-        float* sums = linv + 2 * kRows;                       // [2][128]
-        if (ok) linv[x * kRows + r] = l > 0.f ? 1.f / l : 0.f;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        float d[64];
-        float sq = 0.f;
+        if (ok) ok = dp_warp_wait(o_done, 0, abort_flag, p.dev_error);
+        // Q is no longer read: it carries each thread's base and sum, and sums of squares
+        constexpr int PARTS = 2 * NB, COLS = D / PARTS;       // columns a thread sends, and finishes
+        float* gm = reinterpret_cast<float*>(Qs);             // [part][128]
+        float* gl = gm + PARTS * kRows;
+        float* sums = gl + PARTS * kRows;
+        float* peer_sums = sums + PARTS * kRows;              // [128], from the other CTA
+        if (ok) {
+            gm[part * kRows + r] = m_used;
+            gl[part * kRows + r] = l;
+        }
+        asm volatile("bar.sync 15, %0;" ::"n"(M::SOFTMAX) : "memory");
+        float scale = 0.f;
         if (ok) {
             tc_fence_after();
-            const float i0v = linv[r];
-            const float i1v = valid ? linv[kRows + r] * __ldg(p.lambda + head) : 0.f;
-            const uint32_t oa = lanes + M::O_COL + x * 64, ob = oa + kCols;
+            float top = -INFINITY, lt = 0.f;
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                uint32_t va[32], vb[32];
-                tmem_ld32(oa + cc * 32, va);
-                tmem_ld32(ob + cc * 32, vb);
-                tmem_wait_ld();
+            for (int k = 0; k < PARTS; ++k) top = fmaxf(top, gm[k * kRows + r]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float v = __uint_as_float(va[e]) * i0v - __uint_as_float(vb[e]) * i1v;
-                    d[cc * 32 + e] = v;
-                    sq = fmaf(v, v, sq);
-                }
+            for (int k = 0; k < PARTS; ++k) {
+                const float mk = gm[k * kRows + r];
+                lt += mk == -INFINITY ? 0.f : gl[k * kRows + r] * ex2((mk - top) * c);
+            }
+            if (valid && lt > 0.f) scale = (map ? __ldg(p.lambda + head) : 1.f) / lt;
+        }
+        cluster_sync_all();                                   // both CTAs' Q and rings are free
+        // the other CTA's half of the columns, [column][row]
+        const uint32_t inbox = cluster_map(smem_u32(ring), map ^ 1);
+        const int col = part * COLS;
+        {
+            uint32_t v[COLS];
+            tmem_ld_cols<COLS>(t_o + (map ^ 1) * D + col, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < COLS; ++e)
+                st_cluster_f32(inbox + ((col + e) * kRows + r) * 4, __uint_as_float(v[e]) * scale);
+        }
+        float d[COLS];
+        float sq = 0.f;
+        tmem_ld_cols<COLS>(t_o + map * D + col, reinterpret_cast<uint32_t*>(d));
+        tmem_wait_ld();
+        cluster_sync_all();
+        {
+            const float* in = reinterpret_cast<const float*>(ring) + col * kRows + r;
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) {
+                const float own = d[e] * scale, theirs = in[e * kRows];
+                d[e] = map ? theirs - own : own - theirs;
+                sq = fmaf(d[e], d[e], sq);
             }
         }
         if (p.normalise) {
-            sums[x * kRows + r] = sq;
-            if constexpr (HV == 2) {
-                const uint32_t to = cluster_map(smem_u32(peer_sums + x * kRows + r), half ^ 1);
-                st_cluster_f32(to, sq);
-                cluster_sync_all();
-            } else {
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-            }
+            sums[part * kRows + r] = sq;
+            asm volatile("bar.sync 15, %0;" ::"n"(M::SOFTMAX) : "memory");
+            sq = 0.f;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) sq += sums[k * kRows + r];
+            if (part == 0) st_cluster_f32(cluster_map(smem_u32(peer_sums + r), map ^ 1), sq);
+            cluster_sync_all();
+            sq += peer_sums[r];                               // both CTAs add the same two numbers
         }
         if (ok && valid) {
-            float scale = p.out_scale;
-            const float* nw = p.norm_weight ? p.norm_weight + half * kCols + x * 64 : nullptr;
-            if (p.normalise) {
-                // the halves' sums in the same order in both CTAs
-                float t = sums[r] + sums[kRows + r];
-                if constexpr (HV == 2) t += peer_sums[r] + peer_sums[kRows + r];
-                scale *= 1.f / sqrtf(t / (2 * D) + p.norm_eps);
-            }
-            const bool weighted = p.normalise && nw != nullptr;
-            float4* dst = reinterpret_cast<float4*>(p.out + (row_x * heads + head) * 2 * D + half * kCols +
-                                                    x * 64);
+            float f = p.out_scale;
+            if (p.normalise) f *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
+            const float* nw = p.normalise && p.norm_weight ? p.norm_weight + map * D + col : nullptr;
+            float4* dst = reinterpret_cast<float4*>(p.out + (row_x * heads + head) * 2 * D + map * D + col);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                float4 v = make_float4(d[e] * scale, d[e + 1] * scale, d[e + 2] * scale, d[e + 3] * scale);
-                if (weighted) {
+            for (int e = 0; e < COLS; e += 4) {
+                float4 v = make_float4(d[e] * f, d[e + 1] * f, d[e + 2] * f, d[e + 3] * f);
+                if (nw) {
                     v.x *= __ldg(nw + e), v.y *= __ldg(nw + e + 1);
                     v.z *= __ldg(nw + e + 2), v.w *= __ldg(nw + e + 3);
                 }
                 dst[e / 4] = v;
             }
         }
-    } else if (warp == 8) {
-        // ----------------------------------------------------- producer --
-        // load ld goes to slot ld % SLOTS once the MMAs that read the slot's previous tile
-        // are done.  Lane gi < 8 looks up the page of the tile's 16-row group gi and issues
-        // its boxes; groups outside lo_first .. pos_last read zeros (past the pool's rows).
+    } else if (warp < kMma) {
+        // ---------------------------------------------------- producers --
+        // One warp for K, one for V: tile j goes to stage j % NS once the MMAs that read the
+        // stage's last tile are done.  Lane gi < 8 looks up the page of the tile's 16-row
+        // group gi (groups outside lo_first .. pos_last read zeros: a place past the pool);
+        // one lane issues the copies, K a box of 16 rows x 64 columns at a time, V one of
+        // 16 rows x both heads (issued by eight lanes box by box, the copies of a tile took
+        // longer than its MMAs).
+        const bool value = warp == kProducer + 1;
+        uint64_t* full = value ? v_full : k_full;
+        uint64_t* empty = value ? v_empty : k_empty;
         const uint64_t pol = l2_normal_policy();
         const int32_t* table = p.tables + (int64_t)b * p.max_pages;
         const int gi = lane & 7, H = 2 * p.Hp;
         pdl_wait_primary();                                   // the chunk's rows are stored
-        int issued = 0;
-        bool aborted = false;
-        for (int j = 0; j < ntiles && !aborted; ++j) {
+        auto lookup = [&](int j) {
             const int key = (kt0 + j) * kKeys + 16 * gi;
-            int y = p.pool_rows, y1 = p.pool_rows;            // this group's rows of head 2h, 2h + 1
-            if (lane < 8 && key <= pos_last && key + 15 >= lo_first) {
-                const int32_t page = __ldg(table + key / p.P);
-                if (page >= 0 && page < p.n_pages) {
-                    y = (int)(((int64_t)page * H + 2 * h) * p.P + key % p.P);
-                    y1 = y + p.P;
+            if (j >= ntiles || lane >= 8 || key > pos_last || key + 15 < lo_first) return -1;
+            const int32_t page = __ldg(table + key / p.P);
+            if (page >= 0 && page < p.n_pages) return (int)page;
+            atomicOr(p.dev_error, PKV_DEVERR_PAGE_ID);
+            return -1;
+        };
+        int issued = 0, next = lookup(0);
+        bool aborted = false;
+        for (int j = 0; j < ntiles; ++j) {
+            const int s = j % NS, page = next;
+            const int slot = ((kt0 + j) * kKeys + 16 * gi) % p.P;
+            next = lookup(j + 1);                             // a tile ahead of its use
+            // K: the group's row of the 2-D pool; V: its page
+            const int at = page < 0 ? (value ? (int)p.n_pages : p.pool_rows)
+                                    : value ? page : (int)(((int64_t)page * H + 2 * h + map) * p.P + slot);
+            int where[8], slots[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                where[k] = __shfl_sync(0xffffffffu, at, k);
+                slots[k] = __shfl_sync(0xffffffffu, slot, k);
+            }
+            if (j >= NS && !dp_warp_wait(&empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_error)) {
+                aborted = true;
+                break;
+            }
+            if (elect_one()) {
+                unsigned char* dst = ring + s * M::STAGE;
+                if (value) {
+                    mbar_arrive_expect_tx(&full[s], M::V_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tma_load_5d(dst + M::Q_BYTES + k * M::V_GROUP, &tmv, 0, slots[k], 0, 2 * h, where[k],
+                                    &full[s], pol);
                 } else {
-                    atomicOr(p.dev_error, PKV_DEVERR_PAGE_ID);
+                    mbar_arrive_expect_tx(&full[s], M::Q_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+#pragma unroll
+                        for (int cc = 0; cc < M::CHUNKS; ++cc)
+                            tma_load_2d(dst + cc * M::COL_BYTES + k * 2048, &tmk, cc * 64, where[k], &full[s],
+                                        pol);
                 }
             }
-#pragma unroll
-            for (int w = 0; w < M::LOADS; ++w) {
-                const int ld = M::LOADS * j + w, s = ld % M::SLOTS;
-                if (ld >= M::SLOTS && !pf_warp_wait(&slot_empty[s], ((ld / M::SLOTS) - 1) & 1,
-                                                    abort_flag, p.dev_error)) {
-                    aborted = true;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&slot_full[s], M::SLOT);
-                __syncwarp();
-                if (lane < 8) {
-                    unsigned char* dst = ring + s * M::SLOT + gi * 2048;
-                    const bool value = w == M::LOADS - 1;
-                    const CUtensorMap* map = value ? &tmv : &tmk;
-#pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        // D = 64: one column of either head; D = 128: both columns of one head
-                        const bool second = D == 64 ? cc == 1 : (value ? half == 1 : w == 1);
-                        tma_load_2d(dst + cc * M::COL_BYTES, map, D == 64 ? 0 : cc * 64, second ? y1 : y,
-                                    &slot_full[s], pol);
-                    }
-                }
-                ++issued;
-            }
+            __syncwarp();
+            ++issued;
         }
         if (lane == 0 && (aborted || *abort_flag)) {
             // let the copies in flight land before the CTA's shared memory goes away
-            for (int ld = issued - M::SLOTS > 0 ? issued - M::SLOTS : 0; ld < issued; ++ld)
-                mbar_wait_bounded(&slot_full[ld % M::SLOTS], (ld / M::SLOTS) & 1, kTcWaitLimitNs);
+            for (int j = max(issued - NS, 0); j < issued; ++j)
+                mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kTcWaitLimitNs);
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------- MMA --
         constexpr uint32_t idS = idesc_bf16(kKeys, false);
-        constexpr uint32_t idO = idesc_bf16(kCols, true);
+        constexpr uint32_t idO = idesc_bf16(2 * D, true);
+        // all 512 columns are this CTA's: they start at column 0
+        constexpr uint32_t tS = 0, tO = M::O_COL;
         const uint32_t q_addr = smem_u32(Qs), ring_addr = smem_u32(ring);
-        constexpr int NL = M::LOADS;
-        auto wait_slot = [&](int ld) {
-            return pf_warp_wait(&slot_full[ld % M::SLOTS], (ld / M::SLOTS) & 1, abort_flag,
-                                p.dev_error);
+        auto wait = [&](uint64_t* bar, int phase) {
+            return dp_warp_wait(bar, phase & 1, abort_flag, p.dev_error);
         };
-        auto ld_k = [&](int j, int x) { return NL * j + (NL == 3 ? x : 0); };
-        auto ld_v = [&](int j) { return NL * j + NL - 1; };
-        auto issue_s = [&](int j, int x) {
-            const uint32_t k_addr = ring_addr + (ld_k(j, x) % M::SLOTS) * M::SLOT +
-                                    (NL == 2 ? x * M::COL_BYTES : 0);
-            const uint64_t da = sw128_desc(q_addr + x * M::Q_BYTES, 16, 1024);
-            const uint64_t db = sw128_desc(k_addr, 16, 1024);
-            const uint32_t d = tmem + M::S_COL + x * kKeys;
+        auto issue_s = [&](int j) {
+            const uint64_t da = sw128_desc(q_addr, 16, 1024);
+            const uint64_t db = sw128_desc(ring_addr + (j % NS) * M::STAGE, 16, 1024);
+            const uint32_t d = tS + (j % NB) * kKeys;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint64_t dk = (uint64_t)(((k >> 2) * M::COL_BYTES + (k & 3) * 32) >> 4);
                 umma_bf16(d, da + dk, db + dk, idS, k > 0);
             }
-            umma_commit(&s_full[x]);
-            // the keys' slot is free once its last reader is done
-            if (NL == 3 || x == 1) umma_commit(&slot_empty[ld_k(j, x) % M::SLOTS]);
+            umma_commit(&s_full[j % NB]);
+            umma_commit(&k_empty[j % NS]);
         };
-        auto issue_pv = [&](int j, int x) {
-            // V is MN-major: two 64-column swizzle atoms COL_BYTES apart, 8-row groups 1024
-            const uint64_t dv =
-                sw128_desc(ring_addr + (ld_v(j) % M::SLOTS) * M::SLOT, M::COL_BYTES, 1024);
-            // P in TMEM: keys 16k .. 16k+15 are P_hi columns 64(k/4) + 8(k%4) .. +7 and the
-            // P_lo columns 32 further on
-            const uint32_t pa = tmem + M::S_COL + x * kKeys;
-            const uint32_t o = tmem + M::O_COL + x * kCols;
+        auto issue_pv = [&](int j) {
+            // V is MN-major: a k-step is one 16-row group, its 64-column swizzle atoms 2048
+            // bytes apart, 8-row groups 1024
+            const uint64_t dv = sw128_desc(ring_addr + (j % NS) * M::STAGE + M::Q_BYTES, 2048, 1024);
+            // P in TMEM: keys 16k .. 16k+15 are P_hi columns 16k .. +7 and the P_lo columns
+            // behind them
+            const uint32_t pa = tS + (j % NB) * kKeys;
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k) {
-                const uint64_t dvk = dv + (uint64_t)((k * 16 * 128) >> 4);
-                const uint32_t ph = pa + (k >> 2) * 64 + (k & 3) * 8;
-                umma_bf16_tmem_a(o, ph, dvk, idO, (j > 0 || k > 0) ? 1u : 0u);
-                umma_bf16_tmem_a(o, ph + 32, dvk, idO, 1u);
+                const uint64_t dvk = dv + (uint64_t)((k * M::V_GROUP) >> 4);
+                const uint32_t ph = pa + k * 16;
+                umma_bf16_tmem_a(tO, ph, dvk, idO, (j > 0 || k > 0) ? 1u : 0u);
+                umma_bf16_tmem_a(tO, ph + 8, dvk, idO, 1u);
             }
+            umma_commit(&pv_done[j % NB]);
+            umma_commit(&v_empty[j % NS]);
         };
         // rows [r0, r1) of tile j's values to zero: slots that no row of the CTA may read can
         // hold anything, and their weight is 0
         auto clear = [&](int j, int r0, int r1) {
-            unsigned char* Vs = ring + (ld_v(j) % M::SLOTS) * M::SLOT;
-            for (int idx = lane; idx < (r1 - r0) * 16; idx += 32) {
-                const int row = r0 + idx / 16, piece = idx % 16;
-                *reinterpret_cast<uint4*>(Vs + (piece >> 3) * M::COL_BYTES + row * 128 + (piece & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            unsigned char* Vs = ring + (j % NS) * M::STAGE + M::Q_BYTES;
+            constexpr int PER = 2 * M::CHUNKS * 8;            // 16-byte pieces of a row
+            for (int idx = lane; idx < (r1 - r0) * PER; idx += 32) {
+                const int row = r0 + idx / PER, piece = idx % PER;
+                *reinterpret_cast<uint4*>(Vs + (row >> 4) * M::V_GROUP + (piece >> 3) * 2048 + (row & 15) * 128 +
+                                          (piece & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
         };
-        bool ok = pf_warp_wait(q_ready, 0, abort_flag, p.dev_error) && wait_slot(ld_k(0, 0)) &&
-                  (NL == 2 || wait_slot(ld_k(0, 1)));
+        bool ok = wait(q_ready, 0);
         bool issued_any = false;
-        if (ok) {
+        for (int j = 0; ok && j < NB && j < ntiles; ++j) {
+            if (!(ok = wait(&k_full[j % NS], j / NS))) break;
             tc_fence_after();
-            if (lane == 0) {
-                issue_s(0, 0);
-                issue_s(0, 1);
-            }
-            issued_any = true;
+            if (elect_one()) issue_s(j);
             __syncwarp();
+            issued_any = true;
         }
         for (int j = 0; ok && j < ntiles; ++j) {
-            const bool more = j + 1 < ntiles;
-            if (!pf_warp_wait(&p_full[0], j & 1, abort_flag, p.dev_error) || !wait_slot(ld_v(j))) {
+            // copies first: they are there early, P comes last
+            const bool end = j + 1 == ntiles;
+            const int k0 = (kt0 + j) * kKeys;
+            if (!wait(&v_full[j % NS], j / NS) ||
+                (j + NB < ntiles && !wait(&k_full[(j + NB) % NS], (j + NB) / NS))) {
                 ok = false;
                 break;
             }
-            const int k0 = (kt0 + j) * kKeys;
-            const int last = !more ? ((pos_last - k0) / 16 + 1) * 16 : 0;    // rows copied, last tile
-            const bool clear_end = !more && t_b - k0 < last;
+            const int last = end ? ((pos_last - k0) / 16 + 1) * 16 : 0;      // rows copied, last tile
+            const bool clear_end = end && t_b - k0 < last;
             const bool clear_start = j == 0 && lo_first > k0;
             if (clear_end || clear_start) {
                 if (clear_end) clear(j, t_b - k0, last);
@@ -536,49 +635,37 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            tc_fence_after();
-            if (lane == 0) issue_pv(j, 0);
-            __syncwarp();
-            if (more) {
-                if (!wait_slot(ld_k(j + 1, 0))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (lane == 0) issue_s(j + 1, 0);
-                __syncwarp();
-            }
-            if (!pf_warp_wait(&p_full[1], j & 1, abort_flag, p.dev_error) ||
-                (more && NL == 3 && !wait_slot(ld_k(j + 1, 1)))) {
+            if (!wait(&p_full[j % NB], j / NB)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (lane == 0) {
-                issue_pv(j, 1);
-                umma_commit(&slot_empty[ld_v(j) % M::SLOTS]);
-                if (more) issue_s(j + 1, 1);
-                else umma_commit(o_done);
+            if (elect_one()) {
+                issue_pv(j);
+                if (end) umma_commit(o_done);
+                if (j + NB < ntiles) issue_s(j + NB);
             }
             __syncwarp();
         }
         if (issued_any && *abort_flag) {
             // MMAs still in flight read shared memory and write TMEM: let them finish
-            if (lane == 0) {
+            if (elect_one()) {
                 umma_commit(drain);
                 mbar_wait_bounded(drain, 0, kTcWaitLimitNs);
             }
             __syncwarp();
         }
     }
-    if constexpr (HV == 2) {
-        // producer and MMA warps join the softmax warps' exchange
-        if (warp >= 8 && p.normalise) cluster_sync_all();
+    if (warp >= kProducer) {
+        // producer and MMA warps join the softmax warps' cluster barriers
+        cluster_sync_all();
+        cluster_sync_all();
+        if (p.normalise) cluster_sync_all();
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMma) {
         tc_fence_after();
         tmem_dealloc(tmem, M::TMEM_COLS);
     }
@@ -601,8 +688,8 @@ cudaError_t launch(const DpParams& p, const void* tmap_k, const void* tmap_v, cu
     std::memcpy(&tmk, tmap_k, sizeof tmk);
     std::memcpy(&tmv, tmap_v, sizeof tmv);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(differential_prefill_tiles(p.B, p.G, p.total_new) * p.Hp * M::HALVES));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(differential_prefill_tiles(p.B, p.G, p.total_new) * p.Hp * 2));
+    cfg.blockDim = dim3(M::THREADS);
     cfg.dynamicSmemBytes = M::SMEM;
     cfg.stream = stream;
     // behind the append: the producer waits for it, everything before runs beside it
@@ -610,14 +697,11 @@ cudaError_t launch(const DpParams& p, const void* tmap_k, const void* tmap_v, cu
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (M::HALVES > 1) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = M::HALVES;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-    }
+    attr[1].id = cudaLaunchAttributeClusterDimension;         // the two maps
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, differential_prefill_kernel<D>, p, tmk, tmv);
 }
 

@@ -348,8 +348,8 @@ cudaError_t launch_differential_chunks(const DifferentialArgs& a, int batch, int
 cudaError_t launch_differential_append(const DifferentialArgs& a, int batch, int64_t total_new,
                                        const int32_t* cu_new, cudaStream_t stream);
 
-// Prefill on the tensor cores (bf16, head width 64 or 128): no scratch.  tmap_k, tmap_v:
-// the layer's CUtensorMaps (host memory).
+// Prefill on the tensor cores (bf16, head width 64 or 128): no scratch.  tmap_k: the
+// layer's 2-D map of the K pool; tmap_v: its 5-D map of the V pool (host memory).
 bool differential_prefill_supported(int dtype, int D, int G);
 
 // Upper bound on the query tiles of a call.

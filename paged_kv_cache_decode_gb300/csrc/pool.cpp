@@ -1379,7 +1379,7 @@ cudaError_t enqueue_diff_prefill(pkv_pool* p, int layer, pkv::DifferentialArgs& 
                                  int64_t total_new, const int32_t* cu_new, cudaStream_t s) {
     if (diff_tensor_prefill(p))
         return pkv::launch_differential_prefill(a, batch, total_new, cu_new, &p->tmap_k[(size_t)layer],
-                                                &p->tmap_v[(size_t)layer], s);
+                                                &p->pair_v[(size_t)layer], s);
     a.q_bf16 = p->dtype == PKV_BF16;
     a.block_tokens = diff_block_tokens(p);
     a.rows = diff_chunk_rows(p);
