@@ -27,13 +27,13 @@
 // d_h columns that that one finishes through distributed shared memory, and both take
 // d = map 0 - map 1, its mean square over all 2 d_h columns, and store their half.
 //
-// Warp roles (256 BUFS + 96 threads): softmax groups (two threads per query row; they
+// Warp roles: BUFS softmax groups (d_h = 64: a thread per query row, d_h = 128: two; they
 // stage Q, write P, rescale O, store the output); two producers, for K and for V (copies of
 // 16-row groups: a group never straddles a page); an MMA warp (allocates TMEM, one
 // thread issues the MMAs and commits).  MMAs and copies are issued under elect.sync: in
 // a branch on the lane number every operand is moved to uniform registers each time, at
 // about 100 cycles an instruction, and that bounded the kernel (4 x 2048 tokens, d_h =
-// 128: 414 us against XXX).
+// 128: 414 us against 325).
 //
 // Bound: the tensor cores (P V twice for the hi and lo parts of the weights, which
 // carry each to about 2^-17; one bf16 part alone would be off by 2^-9).  O accumulates
@@ -85,21 +85,15 @@ __device__ __forceinline__ bool dp_warp_wait(uint64_t* bar, uint32_t parity, vol
     return __all_sync(0xffffffffu, ok);
 }
 
-// 16 or 32 consecutive 32-bit columns of this thread's TMEM lane.
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-    if constexpr (N == 32) {
-        tmem_ld32(taddr, r);
-    } else {
-        static_assert(N == 16, "16 or 32 columns");
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-              "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr));
-    }
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -124,8 +118,11 @@ __device__ __forceinline__ bool elect_one() {
 
 template <int D>
 struct DpGeo {
-    static constexpr int BUFS = 2;                           // S buffers = softmax groups
-    static constexpr int SOFTMAX = 256 * BUFS;               // softmax threads
+    // S buffers = softmax groups, and threads of a group that share a row.  (At d_h = 64 TMEM
+    // has room for three buffers, but then registers for one thread a row only: 545 us
+    // against 463 for 2 x ~4000 tokens.)
+    static constexpr int BUFS = 2, SPLIT = 2;
+    static constexpr int SOFTMAX = 128 * SPLIT * BUFS;       // softmax threads
     static constexpr int THREADS = SOFTMAX + 96;             // and two producer warps, the MMA warp
     static constexpr int CHUNKS = D / 64;                    // 128-byte swizzle columns of Q, K
     static constexpr int COL_BYTES = kKeys * 128;            // one such column of 128 rows
@@ -136,7 +133,8 @@ struct DpGeo {
     static constexpr int BAR_BYTES = 256;
     // the rows' exponent bases (this tile's and the last one's), and either key half's
     // maximum for each group, all bf16
-    static constexpr int ROW_BYTES = (2 + 2 * BUFS) * kRows * 2;
+    static constexpr int ROW_BYTES = (2 + SPLIT * BUFS) * kRows * 2;
+    static constexpr int OUT_PITCH = D + 4;                  // floats of an output row in shared memory
     static constexpr int FIXED = 1024 + Q_BYTES + BAR_BYTES + ROW_BYTES;
     static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE < 4 ? (227 * 1024 - FIXED) / STAGE : 4;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
@@ -144,8 +142,9 @@ struct DpGeo {
     static_assert(D == 64 || D == 128, "head width 64 or 128");
     static_assert(BUFS * kKeys <= (int)O_COL, "S buffers and O fill TMEM");
     static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "CTA does not fit an SM");
-    static_assert((4 * STAGES + 3 * BUFS + 3) * 8 + 16 <= BAR_BYTES, "barrier area");
-    static_assert(STAGES * STAGE >= kRows * D * 4, "the other CTA's columns go over the ring");
+    static_assert((4 * STAGES + 3 * BUFS + 3) * 8 + 28 <= BAR_BYTES, "barrier area");
+    static_assert(STAGES * STAGE >= kRows * (D + OUT_PITCH) * 4, "the output goes over the ring");
+    static_assert(kRows % (SOFTMAX / 32 * (128 / D)) == 0, "whole steps of the output rows");
 };
 
 struct DpParams {
@@ -231,7 +230,7 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     uint64_t* drain = q_ready + 1;               // MMA completion on the abort path
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* tile_s = const_cast<int*>(abort_flag) + 1;           // request, tile
+    int* tile_s = const_cast<int*>(abort_flag) + 1;           // request, tile, its cu_new, length
     __nv_bfloat16* base_s =
         reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(bars) + M::BAR_BYTES);   // [2][128]
     __nv_bfloat16* row_max = base_s + 2 * kRows;                                     // [group][half][128]
@@ -248,6 +247,11 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         if (lane == 0) {
             tile_s[0] = it.x;
             tile_s[1] = it.y;
+            if (it.x >= 0) {
+                tile_s[2] = cu_at(p, it.x);
+                tile_s[3] = cu_at(p, it.x + 1);
+                tile_s[4] = len_at(p, it.x);
+            }
             *abort_flag = (*reinterpret_cast<volatile unsigned*>(p.dev_error) & PKV_DEVERR_TIMEOUT) ? 1 : 0;
         }
     }
@@ -255,7 +259,7 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         for (int s = 0; s < 4 * NS; ++s) mbar_init(&bars[s], 1);
         for (int b = 0; b < NB; ++b) {
             mbar_init(&s_full[b], 1);
-            mbar_init(&p_full[b], 256);
+            mbar_init(&p_full[b], 128 * M::SPLIT);
             mbar_init(&pv_done[b], 1);
         }
         mbar_init(o_done, 1);
@@ -273,8 +277,8 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     const uint32_t tmem = *tmem_slot;
 
     const int G = p.G, T = kRows / G;
-    const int c0 = cu_at(p, b), n = cu_at(p, b + 1) - c0;
-    const int t_b = len_at(p, b), L0 = t_b - n;
+    const int c0 = tile_s[2], n = tile_s[3] - c0;
+    const int t_b = tile_s[4], L0 = t_b - n;
     const int i0 = tile_s[1] * T, i_end = min(n, i0 + T);
     const int pos_last = L0 + i_end - 1;
     const int lo_first = p.window > 0 && L0 + i0 + 1 > p.window ? (int)(L0 + i0 + 1 - p.window) : 0;
@@ -282,22 +286,29 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
 
     if (warp < kProducer) {
         // ------------------------------------------------------ softmax --
-        const int grp = warp >> 3;                            // takes tiles grp, grp + NB, ...
-        const int kh = (warp >> 2) & 1;                       // keys 64 kh .. 64 kh + 63 of them
+        constexpr int SP = M::SPLIT, PARTS = SP * NB, KEYS = kKeys / SP;
+        const int grp = warp / (4 * SP);                      // takes tiles grp, grp + NB, ...
+        const int kh = SP == 2 ? (warp >> 2) & 1 : 0;         // keys KEYS kh .. + KEYS - 1 of them
         const int r = threadIdx.x & 127;                      // row of the tile = TMEM lane
         const int g = r % G, i = i0 + r / G;
         const bool valid = i < i_end;
         const int heads = p.Hp * G, head = h * G + g;
         const int64_t row_x = (int64_t)c0 + i;
-        const int part = grp * 2 + kh;
+        const int part = grp * SP + kh;
+        const float weight = map ? __ldg(p.lambda + head) : 1.f;
         {
             const uint4* src =
                 reinterpret_cast<const uint4*>(p.q + ((row_x * heads + head) * 2 + map) * D);
+            uint4 v[(D / 8 + PARTS - 1) / PARTS];
 #pragma unroll
-            for (int u = 0; u < D / 8 / (2 * NB); ++u) {
-                const int piece = part * (D / 8 / (2 * NB)) + u;
-                const uint4 v = valid ? __ldg(src + piece) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(Qs + sw_off(r, piece)) = v;
+            for (int u = 0; u * PARTS < D / 8; ++u) {
+                const int piece = u * PARTS + part;
+                v[u] = valid && piece < D / 8 ? __ldg(src + piece) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u * PARTS < D / 8; ++u) {
+                const int piece = u * PARTS + part;
+                if (piece < D / 8) *reinterpret_cast<uint4*>(Qs + sw_off(r, piece)) = v[u];
             }
         }
         fence_proxy_async_smem();
@@ -308,16 +319,16 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         const int lo = p.window > 0 && pos + 1 > p.window ? (int)(pos + 1 - p.window) : 0;
         const float c = p.scale_log2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = lanes + grp * kKeys + kh * 64;
+        const uint32_t t_s = lanes + grp * kKeys + kh * KEYS;
         const uint32_t t_o = lanes + M::O_COL;
-        // A named barrier for each group and row quarter: the two warps of tile j meet, and
-        // the two of tile j - 1 have arrived with its base (before tile 0: the last group).
+        // A named barrier for each group and row quarter: the SPLIT warps of tile j meet, and
+        // those of tile j - 1 have arrived with its base (before tile 0: the last group).
         const int bar_in = 1 + grp * 4 + (warp & 3), bar_out = 1 + (grp + 1) % NB * 4 + (warp & 3);
         __nv_bfloat16* mine = row_max + part * kRows + r;
         const __nv_bfloat16* other = row_max + (part ^ 1) * kRows + r;
         if (grp == NB - 1) {
             if (kh == 0) base_s[kRows + r] = __float2bfloat16_rn(-INFINITY);
-            asm volatile("bar.arrive %0, 128;" ::"r"(bar_out) : "memory");
+            asm volatile("bar.arrive %0, %1;" ::"r"(bar_out), "n"(64 * SP) : "memory");
         }
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
@@ -325,9 +336,9 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             if (!dp_warp_wait(&s_full[grp], (j / NB) & 1, abort_flag, p.dev_error)) ok = false;
             tc_fence_after();
             // keys e_lo .. e_hi of this half are this row's (none when e_lo > e_hi)
-            const int k0 = (kt0 + j) * kKeys + kh * 64;
-            const bool full = k0 >= lo && k0 + 63 <= hi;
-            const int e_lo = max(lo - k0, 0), e_hi = min(hi - k0, 63);
+            const int k0 = (kt0 + j) * kKeys + kh * KEYS;
+            const bool full = k0 >= lo && k0 + KEYS - 1 <= hi;
+            const int e_lo = max(lo - k0, 0), e_hi = min(hi - k0, KEYS - 1);
             auto load = [&](uint32_t* sv, int chunk) {
                 tmem_ld32(t_s + chunk * 32, sv);
                 tmem_wait_ld();
@@ -340,7 +351,7 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             // S is read twice, 32 columns at a time: for the maximum, then for the weights
             float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int chunk = 0; chunk < 2; ++chunk) {
+            for (int chunk = 0; chunk < KEYS / 32; ++chunk) {
                 uint32_t sv[32];
                 load(sv, chunk);
 #pragma unroll
@@ -353,14 +364,15 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             // of a row take the same.  (The other warp has read `mine` of this group's last
             // tile before it arrived on p_full, without which this S would not be there.)
             const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(m2[0], m2[1]));
-            *mine = own;
-            asm volatile("bar.sync %0, 128;" ::"r"(bar_in) : "memory");
-            const float mx = fmaxf(__bfloat162float(own), __bfloat162float(*other));
+            if constexpr (SP == 2) *mine = own;
+            asm volatile("bar.sync %0, %1;" ::"r"(bar_in), "n"(64 * SP) : "memory");
+            float mx = __bfloat162float(own);
+            if constexpr (SP == 2) mx = fmaxf(mx, __bfloat162float(*other));
             const float before = __bfloat162float(base_s[((j + 1) & 1) * kRows + r]);    // of tile j - 1
             const float base =
                 mx > before && (before == -INFINITY || (mx - before) * c > 8.f) ? mx : before;
             if (kh == 0) base_s[(j & 1) * kRows + r] = __float2bfloat16_rn(base);
-            if (j + 1 < ntiles) asm volatile("bar.arrive %0, 128;" ::"r"(bar_out) : "memory");
+            if (j + 1 < ntiles) asm volatile("bar.arrive %0, %1;" ::"r"(bar_out), "n"(64 * SP) : "memory");
             // l is this thread's share, at the base of its last tile
             if (base != m_used) l *= m_used == -INFINITY ? 0.f : ex2((m_used - base) * c);
             m_used = base;
@@ -371,14 +383,15 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
                     ok = false;
                 tc_fence_after();
 #pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {         // half of O's columns a warp
+                for (int cc = 0; cc < 2 * D / SP / 32; ++cc) {        // its share of O's columns
+                    const uint32_t at = t_o + kh * (2 * D / SP) + cc * 32;
                     uint32_t ov[32];
-                    tmem_ld32(t_o + kh * D + cc * 32, ov);
+                    tmem_ld32(at, ov);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                    tmem_st32(t_o + kh * D + cc * 32, ov);
+                    tmem_st32(at, ov);
                 }
                 tmem_wait_st();
             }
@@ -386,7 +399,7 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             const float2 c2 = make_float2(c, c), nmb2 = make_float2(-mb, -mb), minus = make_float2(-1.f, -1.f);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int chunk = 0; chunk < 2; ++chunk) {
+            for (int chunk = 0; chunk < KEYS / 32; ++chunk) {
                 uint32_t sv[32];
                 load(sv, chunk);
 #pragma unroll
@@ -415,10 +428,9 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         }
         if (ok) ok = dp_warp_wait(o_done, 0, abort_flag, p.dev_error);
         // Q is no longer read: it carries each thread's base and sum, and sums of squares
-        constexpr int PARTS = 2 * NB, COLS = D / PARTS;       // columns a thread sends, and finishes
         float* gm = reinterpret_cast<float*>(Qs);             // [part][128]
         float* gl = gm + PARTS * kRows;
-        float* sums = gl + PARTS * kRows;
+        float* sums = gl + PARTS * kRows;                     // [part][128]
         float* peer_sums = sums + PARTS * kRows;              // [128], from the other CTA
         if (ok) {
             gm[part * kRows + r] = m_used;
@@ -436,58 +448,82 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
                 const float mk = gm[k * kRows + r];
                 lt += mk == -INFINITY ? 0.f : gl[k * kRows + r] * ex2((mk - top) * c);
             }
-            if (valid && lt > 0.f) scale = (map ? __ldg(p.lambda + head) : 1.f) / lt;
+            if (valid && lt > 0.f) scale = weight / lt;
         }
         cluster_sync_all();                                   // both CTAs' Q and rings are free
-        // the other CTA's half of the columns, [column][row]
-        const uint32_t inbox = cluster_map(smem_u32(ring), map ^ 1);
+        // Each CTA finishes the d_h columns of head 2h + map: what it has of the others goes to
+        // the other CTA, as [column][row] (lanes side by side: stores of a lane's own 16 bytes
+        // took distributed shared memory 2.5 times as long)
+        constexpr int COLS = D / PARTS;                       // columns a thread sends, and finishes
         const int col = part * COLS;
-        {
-            uint32_t v[COLS];
-            tmem_ld_cols<COLS>(t_o + (map ^ 1) * D + col, v);
+        const uint32_t inbox = cluster_map(smem_u32(ring), map ^ 1);
+#pragma unroll
+        for (int cc = 0; cc < COLS; cc += 16) {
+            uint32_t v[16];
+            tmem_ld16(t_o + (map ^ 1) * D + col + cc, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < COLS; ++e)
-                st_cluster_f32(inbox + ((col + e) * kRows + r) * 4, __uint_as_float(v[e]) * scale);
+            for (int e = 0; e < 16; ++e)
+                st_cluster_f32(inbox + ((col + cc + e) * kRows + r) * 4, __uint_as_float(v[e]) * scale);
         }
         float d[COLS];
-        float sq = 0.f;
-        tmem_ld_cols<COLS>(t_o + map * D + col, reinterpret_cast<uint32_t*>(d));
+#pragma unroll
+        for (int cc = 0; cc < COLS; cc += 16)
+            tmem_ld16(t_o + map * D + col + cc, reinterpret_cast<uint32_t*>(d) + cc);
         tmem_wait_ld();
         cluster_sync_all();
+        float sq = 0.f;
         {
             const float* in = reinterpret_cast<const float*>(ring) + col * kRows + r;
+            const float f = map ? -scale : scale, g0 = map ? 1.f : -1.f;      // map 0 less map 1
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
-                const float own = d[e] * scale, theirs = in[e * kRows];
-                d[e] = map ? theirs - own : own - theirs;
+                d[e] = fmaf(g0, in[e * kRows], d[e] * f);
                 sq = fmaf(d[e], d[e], sq);
             }
         }
+        // the rows to shared memory, [row][OUT_PITCH], to be stored a row a warp
+        float* rows = reinterpret_cast<float*>(ring) + D * kRows;
+#pragma unroll
+        for (int e = 0; e < COLS; e += 4)
+            *reinterpret_cast<float4*>(rows + r * M::OUT_PITCH + col + e) =
+                make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+        sums[part * kRows + r] = sq;
+        asm volatile("bar.sync 15, %0;" ::"n"(M::SOFTMAX) : "memory");
+        float total = 0.f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) total += sums[k * kRows + r];
         if (p.normalise) {
-            sums[part * kRows + r] = sq;
-            asm volatile("bar.sync 15, %0;" ::"n"(M::SOFTMAX) : "memory");
-            sq = 0.f;
-#pragma unroll
-            for (int k = 0; k < PARTS; ++k) sq += sums[k * kRows + r];
-            if (part == 0) st_cluster_f32(cluster_map(smem_u32(peer_sums + r), map ^ 1), sq);
+            if (part == 0) st_cluster_f32(cluster_map(smem_u32(peer_sums + r), map ^ 1), total);
             cluster_sync_all();
-            sq += peer_sums[r];                               // both CTAs add the same two numbers
         }
-        if (ok && valid) {
+        if (part == 0) {
             float f = p.out_scale;
-            if (p.normalise) f *= 1.f / sqrtf(sq / (2 * D) + p.norm_eps);
-            const float* nw = p.normalise && p.norm_weight ? p.norm_weight + map * D + col : nullptr;
-            float4* dst = reinterpret_cast<float4*>(p.out + (row_x * heads + head) * 2 * D + map * D + col);
+            // (both CTAs add the same two numbers)
+            if (p.normalise) f *= 1.f / sqrtf((total + peer_sums[r]) / (2 * D) + p.norm_eps);
+            gm[r] = f;
+            reinterpret_cast<int*>(gl)[r] =                   // output row of this tile row, or -1
+                ok && valid ? (i - i0) * heads + head : -1;
+        }
+        asm volatile("bar.sync 15, %0;" ::"n"(M::SOFTMAX) : "memory");
+        // a lane 4 columns of a row, LPR lanes a row
+        constexpr int LPR = D / 4, RPW = 32 / LPR, STEP = M::SOFTMAX / 32 * RPW;
+        const int at = lane % LPR * 4;
+        float4 nw = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (p.normalise && p.norm_weight) {
+            const float* w = p.norm_weight + map * D + at;
+            nw = make_float4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+        }
+        float* dst = p.out + ((int64_t)c0 + i0) * heads * 2 * D + map * D + at;
 #pragma unroll
-            for (int e = 0; e < COLS; e += 4) {
-                float4 v = make_float4(d[e] * f, d[e + 1] * f, d[e + 2] * f, d[e + 3] * f);
-                if (nw) {
-                    v.x *= __ldg(nw + e), v.y *= __ldg(nw + e + 1);
-                    v.z *= __ldg(nw + e + 2), v.w *= __ldg(nw + e + 3);
-                }
-                dst[e / 4] = v;
-            }
+        for (int k = 0; k < kRows / STEP; ++k) {
+            const int rr = warp * RPW + lane / LPR + k * STEP;
+            const int row = reinterpret_cast<const int*>(gl)[rr];
+            const float f = gm[rr];
+            const float4 x = *reinterpret_cast<const float4*>(rows + rr * M::OUT_PITCH + at);
+            if (row >= 0)
+                *reinterpret_cast<float4*>(dst + (int64_t)row * 2 * D) =
+                    make_float4(x.x * f * nw.x, x.y * f * nw.y, x.z * f * nw.z, x.w * f * nw.w);
         }
     } else if (warp < kMma) {
         // ---------------------------------------------------- producers --
@@ -504,20 +540,25 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         const int32_t* table = p.tables + (int64_t)b * p.max_pages;
         const int gi = lane & 7, H = 2 * p.Hp;
         pdl_wait_primary();                                   // the chunk's rows are stored
+        // this lane's table entry for tile j, or -1 where nothing is to be read; looked at a
+        // tile later, so that no copy waits for the load
         auto lookup = [&](int j) {
             const int key = (kt0 + j) * kKeys + 16 * gi;
-            if (j >= ntiles || lane >= 8 || key > pos_last || key + 15 < lo_first) return -1;
-            const int32_t page = __ldg(table + key / p.P);
-            if (page >= 0 && page < p.n_pages) return (int)page;
-            atomicOr(p.dev_error, PKV_DEVERR_PAGE_ID);
-            return -1;
+            const bool used = j < ntiles && lane < 8 && key <= pos_last && key + 15 >= lo_first;
+            return used ? __ldg(table + key / p.P) : -2;
         };
-        int issued = 0, next = lookup(0);
+        int issued = 0;
+        int32_t next = lookup(0);
         bool aborted = false;
         for (int j = 0; j < ntiles; ++j) {
-            const int s = j % NS, page = next;
+            const int s = j % NS;
+            int32_t page = next;
+            next = lookup(j + 1);
+            if (page != -2 && (page < 0 || page >= p.n_pages)) {
+                atomicOr(p.dev_error, PKV_DEVERR_PAGE_ID);
+                page = -2;
+            }
             const int slot = ((kt0 + j) * kKeys + 16 * gi) % p.P;
-            next = lookup(j + 1);                             // a tile ahead of its use
             // K: the group's row of the 2-D pool; V: its page
             const int at = page < 0 ? (value ? (int)p.n_pages : p.pool_rows)
                                     : value ? page : (int)(((int64_t)page * H + 2 * h + map) * p.P + slot);
