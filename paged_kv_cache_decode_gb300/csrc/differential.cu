@@ -824,9 +824,10 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
 // as they are: tensor cores would take each operand in three parts).  A stage holds a
 // tile of KT positions as TMA leaves it, K then V: [head][32-column chunk][KT rows][128
 // bytes], 128-byte swizzle (one box of a 5-D map for both heads).
-//   scores   lane (key, part): one key's dot products over D * KT / 32 features of both
-//            maps -- the swizzle spreads 8 keys' 16-byte pieces over all banks, queries
-//            come from shared memory as broadcasts -- then 5 - log2(KT) shuffles
+//   scores   lane (s, part): the dot products of keys s and s + KT/2 over D * KT / 64
+//            features of both maps -- the swizzle spreads 8 keys' 16-byte pieces over all
+//            banks, queries come from shared memory as broadcasts for both keys -- then
+//            a transposed butterfly over the parts that leaves a lane one key of one map
 //   weights  one exponential a lane and row (map lane / 16), through shared memory
 //   values   a lane owns 4 or 8 of the 2 D columns for all rows and both maps: V is read
 //            once, weights as broadcasts; packed two-lane FMAs
@@ -841,7 +842,8 @@ struct F32Geo {
     static constexpr int FIT = kRingBudget / (2 * STAGE_BYTES);
     static constexpr int WARPS = FIT < 12 ? FIT : 12;
     static constexpr int STAGES = kRingBudget / (WARPS * STAGE_BYTES);
-    static constexpr int PARTS = 32 / KT;                  // lanes that share a key
+    static constexpr int KS = KT / 2;                      // a lane takes keys s and s + KS
+    static constexpr int PARTS = 32 / KS;                  // lanes that share the two
     static constexpr int PIECES = D / 4 / PARTS;           // 16-byte pieces of one lane's part
     static constexpr int NV = 2 * D / 128;                 // 4-column vectors of a lane
     static constexpr int Q_BYTES = R * 2 * D * 4, P_BYTES = R * 2 * KT * 4;
@@ -913,7 +915,16 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
     int ahead = 0;                                  // tiles staged and not yet used
     for (; ahead < stages && prod.f < share.end; ++ahead) issue(ahead);
 
-    const int key = lane % KT, quarter = lane / KT, half = lane >> 4;
+    // dot products of keys slot and slot + KS; then the score of key `key` of map `half`
+    const int slot_k = lane % M::KS, part = lane / M::KS, half = lane >> 4, upper = (lane >> 3) & 1;
+    const int key = slot_k + upper * M::KS;
+    const bool writes = KT == 16 || (lane & 4) == 0;          // KT = 8: lanes l, l ^ 4 hold the same
+    auto over_keys = [](float x, auto f) {
+        x = f(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = f(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        if constexpr (KT == 16) x = f(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        return f(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    };
     // 16-byte piece u of key row `key` and head hd is at hd * HEAD + (u / 8) * KT * 128 +
     // key * 128 + ((u % 8) ^ (key % 8)) * 16
     auto piece_at = [](int hd, int u, int row) {
@@ -998,36 +1009,42 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
             }
             float sc[R];                            // this half's map, key `key`
             {
-                float2 d[R][2];
+                float2 d[R][2][2];                  // [row][map][key]
 #pragma unroll
                 for (int mm = 0; mm < 2; ++mm) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) d[r][mm] = make_float2(0.f, 0.f);
+                    for (int r = 0; r < R; ++r) d[r][mm][0] = d[r][mm][1] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int u = 0; u < M::PIECES; ++u) {
-                        const int pu = quarter * M::PIECES + u;
-                        const float4 kv =
-                            *reinterpret_cast<const float4*>(stage + piece_at(mm, pu, key));
+                        const int pu = part * M::PIECES + u;
+                        float4 kv[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            kv[i] = *reinterpret_cast<const float4*>(stage + piece_at(mm, pu, slot_k + i * M::KS));
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const float4 qv =
                                 reinterpret_cast<const float4*>(qs + (r * 2 + mm) * D)[pu];
-                            d[r][mm] = __ffma2_rn(lo2(qv), lo2(kv), d[r][mm]);
-                            d[r][mm] = __ffma2_rn(hi2(qv), hi2(kv), d[r][mm]);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                d[r][mm][i] = __ffma2_rn(lo2(qv), lo2(kv[i]), d[r][mm][i]);
+                                d[r][mm][i] = __ffma2_rn(hi2(qv), hi2(kv[i]), d[r][mm][i]);
+                            }
                         }
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float a = d[r][0].x + d[r][0].y, b = d[r][1].x + d[r][1].y;
+                    // lanes of the other half want the other map, lanes l ^ 8 the other key
+                    float v[2];
 #pragma unroll
-                    for (int o = KT; o <= 8; o <<= 1) {
-                        a += __shfl_xor_sync(0xffffffffu, a, o);
-                        b += __shfl_xor_sync(0xffffffffu, b, o);
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = d[r][0][i].x + d[r][0][i].y, b = d[r][1][i].x + d[r][1][i].y;
+                        v[i] = (half ? b : a) + __shfl_xor_sync(0xffffffffu, half ? a : b, 16);
                     }
-                    // lanes of the other half hold the rest: send them the map they want
-                    const float mine = half ? b : a, other = half ? a : b;
-                    sc[r] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+                    float x = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 8);
+                    if constexpr (KT == 8) x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    sc[r] = x;
                 }
             }
             bool moved = false;
@@ -1035,9 +1052,7 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (k0 + key < r_start[r] || k0 + key >= r_end[r]) sc[r] = -INFINITY;
-                float mx = sc[r];
-#pragma unroll
-                for (int o = 1; o < KT; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mx = over_keys(sc[r], [](float a, float b) { return fmaxf(a, b); });
                 alpha[r] = 1.f;
                 if (mx > m[r] + 8.f || (m[r] == -INFINITY && mx > m[r])) {
                     alpha[r] = exp2f(m[r] - mx);    // 0 for the first
@@ -1046,7 +1061,7 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
                 }
                 const float pr = exp2f(sc[r] - (m[r] == -INFINITY ? 0.f : m[r]));
                 l[r] = fmaf(l[r], alpha[r], pr);
-                if (KT == 16 || (quarter & 1) == 0) pw[(r * 2 + half) * KT + key] = pr;
+                if (writes) pw[(r * 2 + half) * KT + key] = pr;
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -1115,9 +1130,7 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
                 int64_t row;
                 int head, st, en;
                 const bool ok = row_at(p, L, r, row, head, st, en);
-                float lt = l[r];
-#pragma unroll
-                for (int o = 1; o < KT; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+                const float lt = over_keys(l[r], [](float a, float b) { return a + b; });
                 if (has_start && has_end) {
                     if (!ok) continue;              // alike in all lanes
                     const float l0 = __shfl_sync(0xffffffffu, lt, 0);
