@@ -143,13 +143,26 @@ __device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& 
     const int nw = nt >> 5;
     stride = (p.B + kPrefix - 1) / kPrefix;
     entries = (p.B + stride - 1) / stride;
-    const int per = (entries + nt - 1) / nt;            // entries of one thread
+    // units of every entry: a thread for each request, or (stride > 1) a warp for each entry
+    for (int e = stride == 1 ? tid : warp; e < entries; e += stride == 1 ? nt : nw) {
+        int64_t n = 0;
+        const int x1 = min((e + 1) * stride, p.B);
+        for (int x = e * stride + (stride == 1 ? 0 : lane); x < x1; x += 32) {
+            n += units_at(p, x);
+            if (blockIdx.x == 0 && !len_ok(p, len_at(p, x))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+        }
+        if (stride > 1) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+        s.pre[e] = n;
+    }
+    __syncthreads();
+    // exclusive prefix: a thread a run of entries
+    const int per = (entries + nt - 1) / nt;
     const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
     int64_t n = 0;
-    for (int x = e0 * stride; x < min(e1 * stride, p.B); ++x) {
-        n += units_at(p, x);
-        if (blockIdx.x == 0 && !len_ok(p, len_at(p, x))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
-    }
+    for (int e = e0; e < e1; ++e) n += s.pre[e];
     int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -164,9 +177,9 @@ __device__ int64_t build_prefix(const DfParams& p, Prefix& s, int& stride, int& 
         total += s.warp_sum[w];
     }
     for (int e = e0; e < e1; ++e) {
+        const int64_t v = s.pre[e];
         s.pre[e] = at;
-        if (e + 1 < e1)
-            for (int x = e * stride; x < (e + 1) * stride; ++x) at += units_at(p, x);
+        at += v;
     }
     if (tid == 0) s.pre[entries] = total;
     __syncthreads();

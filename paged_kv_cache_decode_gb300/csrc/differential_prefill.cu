@@ -174,35 +174,58 @@ __device__ __forceinline__ int len_at(const DpParams& p, int b) {
 }
 
 // One warp: the query tile that is number `item` of the call -- requests in order, each
-// request's last (heaviest) tile first -- as (request, tile), or (-1, 0) past the last.
-__device__ int2 find_tile(const DpParams& p, int item, bool report) {
+// request's last (heaviest) tile first -- as (request, tile), or (-1, 0) past the last.  A
+// lane looks at 8 requests at a time.  `report`: set the error bit of requests whose
+// lengths do not fit, and of more tiles than the launch has room for (`items`).
+__device__ int2 find_tile(const DpParams& p, int item, int items, bool report) {
+    constexpr int PER = 8;
     const int lane = threadIdx.x & 31, T = kRows / p.G;
-    int before = 0;
-    for (int base = 0; base < p.B; base += 32) {
-        const int b = base + lane;
-        int tiles = 0;
-        if (b < p.B) {
-            const int64_t c0 = cu_at(p, b), c1 = cu_at(p, b + 1), t = len_at(p, b);
+    const int per = p.B <= 32 ? 1 : PER;        // requests of a lane
+    int64_t before = 0;
+    for (int base = 0; base < p.B; base += 32 * per) {
+        const int b0 = base + lane * per;
+        int cu[PER + 1], len[PER], tiles[PER], sum = 0;
+        cu[0] = b0 < p.B ? cu_at(p, b0) : 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            tiles[k] = 0;
+            if (k >= per) continue;
+            cu[k + 1] = b0 + k < p.B ? cu_at(p, b0 + k + 1) : 0;
+            len[k] = b0 + k < p.B ? len_at(p, b0 + k) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (k >= per || b0 + k >= p.B) continue;
+            const int64_t c0 = cu[k], c1 = cu[k + 1], t = len[k];
             const bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.total_new && t - (c1 - c0) >= 0 &&
                             t <= (int64_t)p.max_pages * p.P;
-            if (ok) tiles = (int)((c1 - c0 + T - 1) / T);
+            if (ok) tiles[k] = (int)((c1 - c0 + T - 1) / T);
             else if (report) atomicOr(p.dev_error, PKV_DEVERR_SEQ_LEN);
+            sum += tiles[k];
         }
-        int incl = tiles;
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        const int first = before + incl - tiles;
-        const unsigned hit = __ballot_sync(0xffffffffu, item >= first && item < first + tiles);
+        int64_t at = before + incl - sum;
+        int2 found = make_int2(-1, 0);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (k >= per) continue;
+            if (item >= at && item < at + tiles[k]) found = make_int2(b0 + k, (int)(tiles[k] - 1 - (item - at)));
+            at += tiles[k];
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, found.x >= 0);
         if (hit && !report) {
             const int src = __ffs(hit) - 1;
-            const int f = __shfl_sync(0xffffffffu, first, src), n = __shfl_sync(0xffffffffu, tiles, src);
-            return make_int2(base + src, n - 1 - (item - f));
+            return make_int2(__shfl_sync(0xffffffffu, found.x, src), __shfl_sync(0xffffffffu, found.y, src));
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
+    // requests whose row ranges overlap
+    if (report && lane == 0 && before > items) atomicOr(p.dev_error, PKV_DEVERR_SEQ_LEN);
     return make_int2(-1, 0);
 }
 
@@ -242,8 +265,9 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     const int unit = blockIdx.x >> 1;
     const int item = unit / p.Hp, h = unit - item * p.Hp;
     if (warp == 0) {
-        if (blockIdx.x == 0) find_tile(p, 0, true);
-        const int2 it = find_tile(p, item, false);
+        const int items = gridDim.x / 2 / p.Hp;
+        if (blockIdx.x == 0) find_tile(p, 0, items, true);
+        const int2 it = find_tile(p, item, items, false);
         if (lane == 0) {
             tile_s[0] = it.x;
             tile_s[1] = it.y;

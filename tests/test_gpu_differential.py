@@ -88,7 +88,31 @@ def test_decode_one_long_request_split_over_the_gpu(dtype):
     checked(Case([33000, 3], 2, 8, 64, dtype=dtype, seed=6))
 
 
-@pytest.mark.parametrize("B", [1024, 1025, 2500])
+@pytest.mark.parametrize("dtype,D,G", [("f32", 64, 1), ("f32", 128, 4), ("bf16", 64, 1), ("bf16", 128, 2),
+                                       ("bf16", 128, 8), ("f32", 16, 1)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_decode_single_requests(dtype, D, G, window):
+    """One request: its lanes run in the warps of one CTA up to a length, over the GPU past it."""
+    for t in (0, 1, 16, 17, 100, 192, 193, 383, 384, 385, 768, 769, 3000):
+        checked(Case([t], 2, G, D, dtype=dtype, seed=t, window=window), f"t={t}")
+
+
+def test_decode_single_request_of_a_bad_length():
+    for dtype in ("f32", "bf16"):
+        c = Case([40], 2, 1, 64, dtype=dtype)
+        try:
+            c.dlens[0] = 41
+            c.run()
+            assert c.pool.device_status_bits() == pkv.PKV_DEVERR_SEQ_LEN
+            c.dlens[0] = 40
+            c.tables[0, 1] = -1
+            c.run()
+            assert c.pool.device_status_bits() == pkv.PKV_DEVERR_PAGE_ID
+        finally:
+            c.close()
+
+
+@pytest.mark.parametrize("B", [512, 513, 1025, 2500])
 def test_decode_large_batches(B):
     lens = np.random.default_rng(B).integers(0, 40, size=B)
     checked(Case(lens, 2, 1, 64, dtype="bf16", seed=B))
@@ -210,6 +234,44 @@ def test_prefill_long_chunk(dtype, D):
 def test_prefill_page_sizes(dtype, P):
     new, cached = [P, 300, 7], [0, P + 5, 2 * P]
     checked(Case(np.add(new, cached), 2, 2, 128, P=P, dtype=dtype, new=new, seed=P))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B", [255, 300, 1500])
+def test_prefill_many_short_requests(dtype, B):
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, 4, size=B)
+    new[-1] = 3
+    checked(Case(new + rng.integers(0, 20, size=B), 2, 1, 64, dtype=dtype, new=new, seed=B))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_maximum_that_grows_tile_by_tile(D):
+    """Keys whose scores grow along the cache move the exponent base again and again, in both
+    maps and at different tiles."""
+    c = Case([1500], 2, 1, D, dtype="bf16", new=[300], seed=7)
+    try:
+        ramp = torch.linspace(0.0, 30.0, 1500, device="cuda")[:, None, None]
+        sign = torch.tensor([1.0, -1.0], device="cuda")[None, :, None]
+        c.K[0] = (c.K[0].float() * 0.1 + ramp * sign / D ** 0.5).bfloat16()
+        c.q = (c.q.float() * 0.1 + 1.0).bfloat16()
+        pos = torch.arange(1200, device="cuda")
+        c.k[c.tables[0, pos // 16].long(), :, pos % 16] = c.K[0][:1200]
+        c.k_new = c.K[0][1200:].contiguous()
+        c.run()
+        c.check()
+    finally:
+        c.close()
+
+
+def test_prefill_reports_overlapping_rows():
+    c = Case([40, 40, 40], 2, 1, 64, dtype="bf16", new=[30, 0, 30], seed=1)
+    try:
+        c.cu.copy_(torch.tensor([0, 30, 10, 60], dtype=torch.int32))        # not ascending
+        c.run()
+        assert c.pool.device_status_bits() == pkv.PKV_DEVERR_SEQ_LEN
+    finally:
+        c.close()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
