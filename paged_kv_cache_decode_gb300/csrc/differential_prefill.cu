@@ -11,12 +11,12 @@
 //     P  = 2^(c S - c base)    softmax warps: TMEM -> registers -> bf16 hi + lo
 //                              back into TMEM over the S columns already read
 //     O += P_hi V + P_lo V     tcgen05.mma, A = P from TMEM, M=128 N=2 d_h K=128
-// with c = log2(e) / sqrt(d_h).  S has BUFS buffers of 128 columns beside O's 2 d_h, and
-// a group of four softmax warps each: S of the next tiles is there before a tile's
-// softmax ends, and the groups' softmaxes overlap -- the softmax of one tile (TMEM round
-// trips, exponentials) takes longer than its MMAs, so with one S a map the tensor
-// cores were 43 % busy.  MMA order P V(j), S(j + BUFS): MMAs of one thread run in issue
-// order, so S overwrites P(j) only after P V(j) has read it.
+// with c = log2(e) / sqrt(d_h).  S has two buffers of 128 columns beside O's 2 d_h, and a
+// group of eight softmax warps each (two threads a row, 64 keys a thread): S of the next
+// tile is there before a tile's softmax ends, and the groups' softmaxes overlap.  The
+// softmax of a tile takes about 2000 cycles, its MMAs 2600 (d_h = 128) or 1300 (64).
+// MMA order P V(j), S(j + 2): MMAs of one thread run in issue order, so S overwrites P(j)
+// only after P V(j) has read it.
 //
 // The groups share one exponent base per row, handed from tile to tile through shared
 // memory as soon as a tile's maximum is known.  It moves only when the maximum grows by
@@ -27,16 +27,19 @@
 // d_h columns that that one finishes through distributed shared memory, and both take
 // d = map 0 - map 1, its mean square over all 2 d_h columns, and store their half.
 //
-// Warp roles: BUFS softmax groups (d_h = 64: a thread per query row, d_h = 128: two; they
-// stage Q, write P, rescale O, store the output); two producers, for K and for V (copies of
-// 16-row groups: a group never straddles a page); an MMA warp (allocates TMEM, one
-// thread issues the MMAs and commits).  MMAs and copies are issued under elect.sync: in
-// a branch on the lane number every operand is moved to uniform registers each time, at
-// about 100 cycles an instruction, and that bounded the kernel (4 x 2048 tokens, d_h =
-// 128: 414 us against 325).
+// Warp roles: 16 softmax warps (they stage Q, write P, rescale O, store the output); two
+// producers, for K and for V (copies of 16-row groups: a group never straddles a page);
+// an MMA warp (allocates TMEM, one thread issues the MMAs and commits).  MMAs and copies
+// are issued under elect.sync, V copies for both heads at once: in a branch on the lane
+// number every operand is moved to uniform registers each time, at about 100 cycles an
+// instruction, and that bounded the kernel (4 x 2048 tokens, d_h = 128: 500 us with both
+// maps in a CTA and 405 us like this, against 335).
 //
-// Bound: the tensor cores (P V twice for the hi and lo parts of the weights, which
-// carry each to about 2^-17; one bf16 part alone would be off by 2^-9).  O accumulates
+// Bound: the tensor cores at d_h = 128 (3250 cycles a key tile for 2560 of MMAs at their
+// nominal rate), the softmax and MMA chain at 64 (2030 cycles); beside that about 20000
+// cycles a CTA for its first copies and its output.  P V runs twice, for the hi and lo
+// parts of the weights, which carry each to about 2^-17; one bf16 part alone would be
+// off by 2^-9.  O accumulates
 // inside the tensor cores, whose additions truncate: 5e-6 off the formula at 4096
 // positions, 2e-5 at 16384.
 //
