@@ -11,33 +11,37 @@
 //     P  = 2^(c S - c base)    softmax warps: TMEM -> registers -> bf16 hi + lo
 //                              back into TMEM over the S columns already read
 //     O += P_hi V + P_lo V     tcgen05.mma, A = P from TMEM, M=128 N=2 d_h K=128
-// with c = log2(e) / sqrt(d_h).  S has two buffers of 128 columns beside O's 2 d_h, and a
-// group of eight softmax warps each (two threads a row, 64 keys a thread): S of the next
-// tile is there before a tile's softmax ends, and the groups' softmaxes overlap.  The
-// softmax of a tile takes about 2000 cycles, its MMAs 2600 (d_h = 128) or 1300 (64).
-// MMA order P V(j), S(j + 2): MMAs of one thread run in issue order, so S overwrites P(j)
-// only after P V(j) has read it.
+// with c = log2(e) / sqrt(d_h).  The softmax of a tile takes about 2000 cycles (two threads
+// a row, 64 keys a thread), its MMAs 2600 (d_h = 128) or 1300 (64): something has to run
+// beside it.
+//   d_h = 128  O takes half of TMEM, so one CTA has the SM.  S has two buffers and a
+//              group of eight softmax warps each: S of the next tile is there before a
+//              tile's softmax ends, and the groups overlap.  They share one exponent base
+//              per row, handed from tile to tile through shared memory as soon as a
+//              tile's maximum is known.
+//   d_h = 64   two CTAs share the SM, one S buffer and one group each.
+// MMA order P V(j), S(j + buffers): MMAs of one thread run in issue order, so S overwrites
+// P(j) only after P V(j) has read it.
 //
-// The groups share one exponent base per row, handed from tile to tile through shared
-// memory as soon as a tile's maximum is known.  It moves only when the maximum grows by
-// more than 8 in log2 units (weights stay below 2^8; O / l uses the same base in both);
-// the group that moves it waits for the previous P V and rescales O.
+// The base moves only when the maximum grows by more than 8 in log2 units (weights stay
+// below 2^8; O / l uses the same base in both); the group that moves it waits for the
+// previous P V and rescales O.
 //
 // At the end CTA m scales its O by 1 / l (map 1: lambda / l), sends the other CTA the
 // d_h columns that that one finishes through distributed shared memory, and both take
 // d = map 0 - map 1, its mean square over all 2 d_h columns, and store their half.
 //
-// Warp roles: 16 softmax warps (they stage Q, write P, rescale O, store the output); two
-// producers, for K and for V (copies of 16-row groups: a group never straddles a page);
-// an MMA warp (allocates TMEM, one thread issues the MMAs and commits).  MMAs and copies
-// are issued under elect.sync, V copies for both heads at once: in a branch on the lane
-// number every operand is moved to uniform registers each time, at about 100 cycles an
-// instruction, and that bounded the kernel (4 x 2048 tokens, d_h = 128: 500 us with both
-// maps in a CTA and 405 us like this, against 335).
+// Warp roles: 16 (8) softmax warps (they stage Q, write P, rescale O, store the output);
+// producers, for K and for V (d_h = 64: one for both; copies of 16-row groups: a group
+// never straddles a page); an MMA warp (allocates TMEM, one thread issues the MMAs and
+// commits).  MMAs and copies are issued under elect.sync, V copies for both heads at
+// once: in a branch on the lane number every operand is moved to uniform registers each
+// time, at about 100 cycles an instruction, and that bounded the kernel (4 x 2048
+// tokens, d_h = 128: 500 us with both maps in a CTA, 405 us like this, against 335).
 //
 // Bound: the tensor cores at d_h = 128 (3250 cycles a key tile for 2560 of MMAs at their
-// nominal rate), the softmax and MMA chain at 64 (2030 cycles); beside that about 20000
-// cycles a CTA for its first copies and its output.  P V runs twice, for the hi and lo
+// nominal rate; beside that about 20000 cycles a CTA for its first copies and its
+// output); at 64 the tensor cores and the exponentials about alike.  P V runs twice, for the hi and lo
 // parts of the weights, which carry each to about 2^-17; one bf16 part alone would be
 // off by 2^-9.  O accumulates
 // inside the tensor cores, whose additions truncate: 5e-6 off the formula at 4096
@@ -121,30 +125,36 @@ __device__ __forceinline__ bool elect_one() {
 
 template <int D>
 struct DpGeo {
-    // S buffers = softmax groups, and threads of a group that share a row.  (At d_h = 64 TMEM
-    // has room for three buffers, but then registers for one thread a row only: 545 us
-    // against 463 for 2 x ~4000 tokens.)
-    static constexpr int BUFS = 2, SPLIT = 2;
+    // S buffers = softmax groups of 128 SPLIT threads.  d_h = 128: one CTA fills an SM (O
+    // alone takes half of TMEM) and hides a tile's softmax behind the other buffer's.
+    // d_h = 64: two CTAs share an SM, one S buffer each -- a CTA's softmax, first copies
+    // and output run beside the other's MMAs (458 us for 2 x ~4000 tokens with one CTA of
+    // two buffers).
+    static constexpr int CTAS = D == 64 ? 2 : 1;
+    static constexpr int BUFS = D == 64 ? 1 : 2, SPLIT = 2;
     static constexpr int SOFTMAX = 128 * SPLIT * BUFS;       // softmax threads
-    static constexpr int THREADS = SOFTMAX + 96;             // and two producer warps, the MMA warp
+    static constexpr int PRODUCERS = D == 64 ? 1 : 2;        // warps: K and V, or one each
+    static constexpr int THREADS = SOFTMAX + 32 * PRODUCERS + 32;
     static constexpr int CHUNKS = D / 64;                    // 128-byte swizzle columns of Q, K
     static constexpr int COL_BYTES = kKeys * 128;            // one such column of 128 rows
     static constexpr int Q_BYTES = CHUNKS * COL_BYTES;       // Q, or the K of a tile
     static constexpr int V_BYTES = 2 * Q_BYTES;              // both heads' V of a tile
     static constexpr int V_GROUP = V_BYTES / 8;              // 16 positions of it
     static constexpr int STAGE = Q_BYTES + V_BYTES;
-    static constexpr int BAR_BYTES = 256;
-    // the rows' exponent bases (this tile's and the last one's), and either key half's
-    // maximum for each group, all bf16
-    static constexpr int ROW_BYTES = (2 + SPLIT * BUFS) * kRows * 2;
+    static constexpr int BAR_BYTES = D == 64 ? 160 : 256;
+    // either key half's maximum for each group and (two groups) the rows' exponent bases of
+    // this tile and the last one, all bf16
+    static constexpr int ROW_BYTES = (SPLIT * BUFS + (BUFS > 1 ? 2 : 0)) * kRows * 2;
     static constexpr int OUT_PITCH = D + 4;                  // floats of an output row in shared memory
-    static constexpr int FIXED = 1024 + Q_BYTES + BAR_BYTES + ROW_BYTES;
-    static constexpr int STAGES = (227 * 1024 - FIXED) / STAGE < 4 ? (227 * 1024 - FIXED) / STAGE : 4;
+    // (dynamic shared memory starts on a 1024-byte boundary; checked)
+    static constexpr int FIXED = Q_BYTES + BAR_BYTES + ROW_BYTES;
+    static constexpr int ROOM = CTAS == 2 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
+    static constexpr int STAGES = (ROOM - FIXED) / STAGE < 4 ? (ROOM - FIXED) / STAGE : 4;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
-    static constexpr uint32_t O_COL = 512 - 2 * D, TMEM_COLS = 512;
+    static constexpr uint32_t O_COL = BUFS * kKeys, TMEM_COLS = 512 / CTAS;
     static_assert(D == 64 || D == 128, "head width 64 or 128");
-    static_assert(BUFS * kKeys <= (int)O_COL, "S buffers and O fill TMEM");
-    static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "CTA does not fit an SM");
+    static_assert(O_COL + 2 * D <= TMEM_COLS, "S buffers and O fill TMEM");
+    static_assert(STAGES >= 2 && SMEM <= ROOM, "CTAs do not fit an SM");
     static_assert((4 * STAGES + 3 * BUFS + 3) * 8 + 28 <= BAR_BYTES, "barrier area");
     static_assert(STAGES * STAGE >= kRows * (D + OUT_PITCH) * 4, "the output goes over the ring");
     static_assert(kRows % (SOFTMAX / 32 * (128 / D)) == 0, "whole steps of the output rows");
@@ -233,14 +243,12 @@ __device__ int2 find_tile(const DpParams& p, int item, int items, bool report) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(DpGeo<D>::THREADS, 1)
+__global__ void __launch_bounds__(DpGeo<D>::THREADS, DpGeo<D>::CTAS)
 differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv) {
     using M = DpGeo<D>;
     constexpr int NB = M::BUFS, NS = M::STAGES;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* sm = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char* Qs = sm;
     unsigned char* ring = Qs + M::Q_BYTES;       // per stage: K, then V of both heads
     uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * M::STAGE);
@@ -257,12 +265,13 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tile_s = const_cast<int*>(abort_flag) + 1;           // request, tile, its cu_new, length
-    __nv_bfloat16* base_s =
-        reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(bars) + M::BAR_BYTES);   // [2][128]
-    __nv_bfloat16* row_max = base_s + 2 * kRows;                                     // [group][half][128]
+    __nv_bfloat16* row_max =
+        reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(bars) + M::BAR_BYTES);
+                                                 // [group][half][128]
+    __nv_bfloat16* base_s = row_max + M::SPLIT * NB * kRows;  // [2][128] (two groups)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kProducer = M::SOFTMAX / 32, kMma = kProducer + 2;
+    constexpr int kProducer = M::SOFTMAX / 32, kMma = kProducer + M::PRODUCERS;
     // CTAs: item-major, then KV pair, then map (a cluster's two CTAs)
     const int map = blockIdx.x & 1;
     const int unit = blockIdx.x >> 1;
@@ -297,6 +306,11 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
     __syncthreads();
     const int b = tile_s[0];
     if (b < 0) return;                           // both CTAs of a cluster alike
+    if (smem_u32(sm) & 1023) {                   // the swizzle's pattern (alike in every CTA; reported
+                                                 // as work that gave up)
+        if (threadIdx.x == 0) atomicOr(p.dev_error, PKV_DEVERR_TIMEOUT);
+        return;
+    }
     if (warp == kMma) tmem_alloc(tmem_slot, M::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -353,7 +367,7 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         const int bar_in = 1 + grp * 4 + (warp & 3), bar_out = 1 + (grp + 1) % NB * 4 + (warp & 3);
         __nv_bfloat16* mine = row_max + part * kRows + r;
         const __nv_bfloat16* other = row_max + (part ^ 1) * kRows + r;
-        if (grp == NB - 1) {
+        if (NB > 1 && grp == NB - 1) {
             if (kh == 0) base_s[kRows + r] = __float2bfloat16_rn(-INFINITY);
             asm volatile("bar.arrive %0, %1;" ::"r"(bar_out), "n"(64 * SP) : "memory");
         }
@@ -391,15 +405,18 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             // of a row take the same.  (The other warp has read `mine` of this group's last
             // tile before it arrived on p_full, without which this S would not be there.)
             const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(m2[0], m2[1]));
-            if constexpr (SP == 2) *mine = own;
-            asm volatile("bar.sync %0, %1;" ::"r"(bar_in), "n"(64 * SP) : "memory");
-            float mx = __bfloat162float(own);
-            if constexpr (SP == 2) mx = fmaxf(mx, __bfloat162float(*other));
-            const float before = __bfloat162float(base_s[((j + 1) & 1) * kRows + r]);    // of tile j - 1
+            *mine = own;
+            constexpr int kMeet = NB > 1 ? 64 * SP : 32 * SP;
+            asm volatile("bar.sync %0, %1;" ::"r"(bar_in), "n"(kMeet) : "memory");
+            const float mx = fmaxf(__bfloat162float(own), __bfloat162float(*other));
+            // the base of tile j - 1: from the other group's warps, or this thread's own
+            const float before = NB > 1 ? __bfloat162float(base_s[((j + 1) & 1) * kRows + r]) : m_used;
             const float base =
                 mx > before && (before == -INFINITY || (mx - before) * c > 8.f) ? mx : before;
-            if (kh == 0) base_s[(j & 1) * kRows + r] = __float2bfloat16_rn(base);
-            if (j + 1 < ntiles) asm volatile("bar.arrive %0, %1;" ::"r"(bar_out), "n"(64 * SP) : "memory");
+            if (NB > 1) {
+                if (kh == 0) base_s[(j & 1) * kRows + r] = __float2bfloat16_rn(base);
+                if (j + 1 < ntiles) asm volatile("bar.arrive %0, %1;" ::"r"(bar_out), "n"(kMeet) : "memory");
+            }
             // l is this thread's share, at the base of its last tile
             if (base != m_used) l *= m_used == -INFINITY ? 0.f : ex2((m_used - base) * c);
             m_used = base;
@@ -554,15 +571,12 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
         }
     } else if (warp < kMma) {
         // ---------------------------------------------------- producers --
-        // One warp for K, one for V: tile j goes to stage j % NS once the MMAs that read the
+        // (d_h = 128: a warp for K, one for V.)  Tile j goes to stage j % NS once the MMAs that read the
         // stage's last tile are done.  Lane gi < 8 looks up the page of the tile's 16-row
         // group gi (groups outside lo_first .. pos_last read zeros: a place past the pool);
         // one lane issues the copies, K a box of 16 rows x 64 columns at a time, V one of
         // 16 rows x both heads (issued by eight lanes box by box, the copies of a tile took
         // longer than its MMAs).
-        const bool value = warp == kProducer + 1;
-        uint64_t* full = value ? v_full : k_full;
-        uint64_t* empty = value ? v_empty : k_empty;
         const uint64_t pol = l2_normal_policy();
         const int32_t* table = p.tables + (int64_t)b * p.max_pages;
         const int gi = lane & 7, H = 2 * p.Hp;
@@ -574,9 +588,9 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             const bool used = j < ntiles && lane < 8 && key <= pos_last && key + 15 >= lo_first;
             return used ? __ldg(table + key / p.P) : -2;
         };
-        int issued = 0;
+        const bool keys = M::PRODUCERS == 1 || warp == kProducer, values = M::PRODUCERS == 1 || !keys;
+        int k_issued = 0, v_issued = 0;
         int32_t next = lookup(0);
-        bool aborted = false;
         for (int j = 0; j < ntiles; ++j) {
             const int s = j % NS;
             int32_t page = next;
@@ -587,51 +601,58 @@ differential_prefill_kernel(const __grid_constant__ DpParams p, const __grid_con
             }
             const int slot = ((kt0 + j) * kKeys + 16 * gi) % p.P;
             // K: the group's row of the 2-D pool; V: its page
-            const int at = page < 0 ? (value ? (int)p.n_pages : p.pool_rows)
-                                    : value ? page : (int)(((int64_t)page * H + 2 * h + map) * p.P + slot);
-            int where[8], slots[8];
+            const int row = page < 0 ? p.pool_rows : (int)(((int64_t)page * H + 2 * h + map) * p.P + slot);
+            if (page < 0) page = (int32_t)p.n_pages;
+            int rows[8], pages[8], slots[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                where[k] = __shfl_sync(0xffffffffu, at, k);
+                rows[k] = __shfl_sync(0xffffffffu, row, k);
+                pages[k] = __shfl_sync(0xffffffffu, page, k);
                 slots[k] = __shfl_sync(0xffffffffu, slot, k);
             }
-            if (j >= NS && !dp_warp_wait(&empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_error)) {
-                aborted = true;
-                break;
-            }
-            if (elect_one()) {
-                unsigned char* dst = ring + s * M::STAGE;
-                if (value) {
-                    mbar_arrive_expect_tx(&full[s], M::V_BYTES);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tma_load_5d(dst + M::Q_BYTES + k * M::V_GROUP, &tmv, 0, slots[k], 0, 2 * h, where[k],
-                                    &full[s], pol);
-                } else {
-                    mbar_arrive_expect_tx(&full[s], M::Q_BYTES);
+            unsigned char* dst = ring + s * M::STAGE;
+            const uint32_t past = ((j / NS) - 1) & 1;
+            if (keys) {
+                if (j >= NS && !dp_warp_wait(&k_empty[s], past, abort_flag, p.dev_error)) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&k_full[s], M::Q_BYTES);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
 #pragma unroll
                         for (int cc = 0; cc < M::CHUNKS; ++cc)
-                            tma_load_2d(dst + cc * M::COL_BYTES + k * 2048, &tmk, cc * 64, where[k], &full[s],
+                            tma_load_2d(dst + cc * M::COL_BYTES + k * 2048, &tmk, cc * 64, rows[k], &k_full[s],
                                         pol);
                 }
+                __syncwarp();
+                ++k_issued;
             }
-            __syncwarp();
-            ++issued;
+            if (values) {
+                if (j >= NS && !dp_warp_wait(&v_empty[s], past, abort_flag, p.dev_error)) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&v_full[s], M::V_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tma_load_5d(dst + M::Q_BYTES + k * M::V_GROUP, &tmv, 0, slots[k], 0, 2 * h, pages[k],
+                                    &v_full[s], pol);
+                }
+                __syncwarp();
+                ++v_issued;
+            }
         }
-        if (lane == 0 && (aborted || *abort_flag)) {
+        if (lane == 0 && (k_issued + v_issued < ((int)keys + (int)values) * ntiles || *abort_flag)) {
             // let the copies in flight land before the CTA's shared memory goes away
-            for (int j = max(issued - NS, 0); j < issued; ++j)
-                mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kTcWaitLimitNs);
+            for (int j = max(k_issued - NS, 0); j < k_issued; ++j)
+                mbar_wait_bounded(&k_full[j % NS], (j / NS) & 1, kTcWaitLimitNs);
+            for (int j = max(v_issued - NS, 0); j < v_issued; ++j)
+                mbar_wait_bounded(&v_full[j % NS], (j / NS) & 1, kTcWaitLimitNs);
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------- MMA --
         constexpr uint32_t idS = idesc_bf16(kKeys, false);
         constexpr uint32_t idO = idesc_bf16(2 * D, true);
-        // all 512 columns are this CTA's: they start at column 0
-        constexpr uint32_t tS = 0, tO = M::O_COL;
+        // a CTA that has all 512 columns has them from column 0: constants
+        const uint32_t tS = M::CTAS == 1 ? 0 : tmem, tO = tS + M::O_COL;
         const uint32_t q_addr = smem_u32(Qs), ring_addr = smem_u32(ring);
         auto wait = [&](uint64_t* bar, int phase) {
             return dp_warp_wait(bar, phase & 1, abort_flag, p.dev_error);
