@@ -230,7 +230,8 @@ int pkv_request_fork(const pkv_request* parent, pkv_request** child);
  * Fork n children of `parent` at once (parallel samples or beams of one prompt):
  * children[0 .. n) receive requests at the parent's visible length that share its
  * full pages.  The partly filled last page, if there is one, is not shared: every
- * child gets a private copy now -- one page each from the free list's front, in
+ * child gets a private copy now (ordered after the parent's own writes on
+ * `stream`) -- one page each from the free list's front, in
  * child order, K and V of all layers copied in one launch on `stream` (one for
  * every 480 children) -- so that no child's first token has to copy it layer by
  * layer.  Pages the parent leased ahead of its length are not shared.  Calls that
@@ -636,9 +637,11 @@ int pkv_differential_prefill_workspace_size(const pkv_pool* pool, int batch, int
  * bf16 pools of head_dim 64 or 128 run on the tcgen05 tensor cores (bf16 products
  * with fp32 accumulation, the weights as bf16 hi + lo; two kernels: append,
  * attention).  Every other pool runs chunk tokens, or blocks of them, as lanes of
- * the decode kernel (four kernels: append, blocks, split, merge).  A request with n_b = 0 appends nothing.  Bad lengths or page ids set the pool's
- * error word; the affected rows are then unspecified, rows at or past
- * cu_new[batch] are left as they were.
+ * the decode kernel (four kernels: append, blocks, split, merge).  A request with
+ * n_b = 0 appends nothing.  Bad lengths or page ids set the pool's error word; the
+ * affected rows are then unspecified, rows at or past cu_new[batch] are left as
+ * they were.  Once a wait has run out (PKV_DEVERR_TIMEOUT), later tensor-core calls
+ * may skip their work until pkv_check_device_status clears the word.
  */
 int pkv_paged_differential_prefill(pkv_pool* pool, int layer, int batch, int64_t total_new,
                                    const void* q, const void* k_new, const void* v_new,

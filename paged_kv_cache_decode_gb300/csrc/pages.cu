@@ -34,28 +34,34 @@ struct CopyParams {
     int64_t layer_bytes, page_bytes, n_pages;
     int layers, n;
     int64_t chunks;                                 // units of one page: kThreads * kUnroll * 16 bytes
-    const int32_t* src;
-    const int32_t* dst;
     unsigned* err;
 };
 
-struct PairList {
+// Where the ids of pair i come from: device lists, or a host list that travels with the
+// launch.
+struct DeviceIds {
+    const int32_t* src;
+    const int32_t* dst;
+    __device__ int2 at(int i) const { return make_int2(__ldg(src + i), __ldg(dst + i)); }
+};
+
+struct ListIds {
     int2 pair[kInlinePairs];
+    __device__ int2 at(int i) const { return pair[i]; }
 };
 
 // One unit per turn: a chunk (16 KB; 8 pieces in flight instead of 4 gain nothing) of one
-// page of one pool.  INLINE: the ids came with the
-// launch (host lists), else from device memory.
-template <bool INLINE>
+// page of one pool.
+template <typename IDS>
 __global__ void __launch_bounds__(kThreads)
-copy_pages_kernel(const __grid_constant__ CopyParams p, const __grid_constant__ PairList list) {
+copy_pages_kernel(const __grid_constant__ CopyParams p, const __grid_constant__ IDS ids) {
     const int64_t units = (int64_t)p.n * p.layers * 2 * p.chunks;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t page_unit = u / p.chunks, chunk = u - page_unit * p.chunks;
         const int64_t pool = page_unit / p.n;
         const int i = (int)(page_unit - pool * p.n);
-        const int src = INLINE ? list.pair[i].x : __ldg(p.src + i);
-        const int dst = INLINE ? list.pair[i].y : __ldg(p.dst + i);
+        const int2 pair = ids.at(i);
+        const int src = pair.x, dst = pair.y;
         if (src < 0 || src >= p.n_pages || dst < 0 || dst >= p.n_pages) {
             if (threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_PAGE_ID);
             continue;
@@ -187,10 +193,8 @@ unsigned copy_grid(const CopyParams& p) {
 
 cudaError_t launch_copy_pages(const PageStore& s, int n, const int32_t* src, const int32_t* dst,
                               cudaStream_t stream) {
-    CopyParams p = copy_params(s, n);
-    p.src = src;
-    p.dst = dst;
-    copy_pages_kernel<false><<<copy_grid(p), kThreads, 0, stream>>>(p, PairList{});
+    const CopyParams p = copy_params(s, n);
+    copy_pages_kernel<<<copy_grid(p), kThreads, 0, stream>>>(p, DeviceIds{src, dst});
     return cudaGetLastError();
 }
 
@@ -198,10 +202,10 @@ cudaError_t launch_copy_page_list(const PageStore& s, int n, const int32_t* src,
                                   cudaStream_t stream) {
     for (int i = 0; i < n; i += kInlinePairs) {
         const int m = n - i < kInlinePairs ? n - i : kInlinePairs;
-        CopyParams p = copy_params(s, m);
-        PairList list{};
+        const CopyParams p = copy_params(s, m);
+        ListIds list{};
         for (int k = 0; k < m; ++k) list.pair[k] = make_int2(src[i + k], dst[i + k]);
-        copy_pages_kernel<true><<<copy_grid(p), kThreads, 0, stream>>>(p, list);
+        copy_pages_kernel<<<copy_grid(p), kThreads, 0, stream>>>(p, list);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

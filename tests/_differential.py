@@ -15,11 +15,11 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 class Case:
     """Requests of lengths `lens` (the new tokens included; `new` of them new, default one
-    each) over one layer of a differential pool whose pages are handed out in a shuffled
-    order; unused slots hold NaN."""
+    each) over one layer of a differential pool whose pages (from `first_page` on) are handed
+    out in a shuffled order; unused slots hold NaN."""
 
     def __init__(self, lens, H, G, D, P=16, dtype="bf16", window=0, new=None, seed=0, layers=1, layer=0,
-                 amp=1.0, max_context=None, table_pad=1, norm=True, weight=True):
+                 amp=1.0, max_context=None, table_pad=1, norm=True, weight=True, first_page=0):
         self.lens = np.asarray(lens, dtype=np.int64)
         self.B, self.H, self.G, self.D, self.P, self.window = len(self.lens), H, G, D, P, window
         self.new = np.asarray(new, dtype=np.int64) if new is not None else None
@@ -31,8 +31,8 @@ class Case:
             return (amp * torch.randn(*shape, generator=g, device="cuda")).to(dtype)
 
         need = -(-self.lens // P)
-        pages = int(need.sum()) + 2
-        perm = rng.permutation(pages)
+        pages = int(need.sum()) + 2 + first_page
+        perm = first_page + rng.permutation(pages - first_page)
         tables = np.full((self.B, int(need.max(initial=0)) + table_pad), -1, np.int32)
         at = 0
         for b, n in enumerate(need):
@@ -122,8 +122,9 @@ class Case:
                 pg = self.tables[b, pos // self.P].long()
                 seen[pg, pos % self.P] = True
                 assert torch.equal(pages[pg, :, pos % self.P], rows[b]), f"{what}: rows of request {b}"
-            rest = pages.transpose(1, 2)[~seen]
-            assert torch.isnan(rest).all(), f"{what}: a slot of nobody was written"
+            if pages.numel() < 1 << 30:
+                rest = pages.transpose(1, 2)[~seen]
+                assert torch.isnan(rest).all(), f"{what}: a slot of nobody was written"
 
     def close(self):
         self.pool.close()

@@ -118,6 +118,14 @@ def test_decode_large_batches(B):
     checked(Case(lens, 2, 1, 64, dtype="bf16", seed=B))
 
 
+@pytest.mark.parametrize("dtype,D,P", [("bf16", 128, 16), ("f32", 64, 32)])
+def test_pages_past_32_bit_offsets(dtype, D, P):
+    """Pages behind more than 2^31 elements of a layer: read, appended to, attended."""
+    first = (1 << 31) // (32 * P * D) + 5
+    checked(Case([P + 3, 200, 1], 32, 1, D, P=P, dtype=dtype, seed=2, first_page=first), "decode")
+    checked(Case([P + 3, 200], 32, 1, D, P=P, dtype=dtype, seed=3, new=[P, 70], first_page=first), "prefill")
+
+
 def test_decode_without_norm_and_without_weight():
     for dtype in ("f32", "bf16"):
         checked(Case([7, 300], 4, 2, 64, dtype=dtype, norm=False))
@@ -179,6 +187,39 @@ def test_decode_on_a_stream_and_two_at_once():
     finally:
         a.close()
         b.close()
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_two_graphs_and_an_eager_call_share_no_scratch(kind):
+    """Scratch made by the call itself: two captured graphs replayed at once on two streams,
+    with an eager call beside them."""
+    new = None if kind == "decode" else [30, 90]
+    cases = [Case([700, 3000 + i], 4, 1, 64, dtype="f32", seed=20 + i, new=new) for i in range(3)]
+    try:
+        for c in cases:
+            c.run()
+        torch.cuda.synchronize()
+        graphs = []
+        for c in cases[:2]:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                c.run()
+            graphs.append(g)
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for c in cases:
+            c.out.fill_(math.nan)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+            cases[2].run()
+        torch.cuda.synchronize()
+        for c in cases:
+            c.check()
+    finally:
+        for c in cases:
+            c.close()
 
 
 @pytest.mark.parametrize("kind", ["decode", "prefill"])

@@ -176,3 +176,95 @@ def test_fork_batch_copies_the_tail_once_for_every_layer(n):
         assert pool.check_device_status() == 0
     finally:
         pool.close()
+
+
+def grown(pool, n, seed=0):
+    """A request of n committed positions, every layer filled by a chunk."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    req = pool.request()
+    req.begin_chunk(n)
+    for l in range(pool.layers):
+        x = lambda h: torch.randn(n, h, pool.head_dim, generator=g, device="cuda").to(pool.torch_dtype)  # noqa: E731
+        req.prefill_chunk(l, x(pool.query_heads), x(pool.heads), x(pool.heads))
+    req.commit_token()
+    return req
+
+
+def rows(pool, req):
+    """Every layer's K and V rows of a request, in order."""
+    t = torch.tensor(req.page_table(), device="cuda")
+    return [x[t].transpose(1, 2).flatten(0, 1)[:req.length].clone() for l in range(pool.layers)
+            for x in pool.kv_pages(l)]
+
+
+def test_request_compact_and_truncate_bookkeeping():
+    pool = pkv.Pool(2, 20, 2, 64, 16, "bf16", 128, seed=4)
+    try:
+        req = grown(pool, 70)
+        kid = req.fork()
+        was, table, free = rows(pool, req), req.page_table(), pool.free_list()
+        keep = torch.arange(1, 70, 3, dtype=torch.int32, device="cuda")
+        before = req.counters()
+        req.compact(keep)
+        assert req.length == 23 and req.counters() == before
+        assert req.page_table() == free[:2]
+        assert [pool.page_refs(p) for p in table] == [1] * 5           # the child's now
+        for x, y in zip(rows(pool, req), was):
+            assert torch.equal(x, y[keep.long()])
+        for x, y in zip(rows(pool, kid), was):
+            assert torch.equal(x, y)
+        kid.truncate(33)
+        assert kid.page_table() == table[:3] and pool.free_list() == free[2:] + table[3:]
+        req.compact(torch.arange(23, dtype=torch.int32, device="cuda"))     # all of them: moved as they are
+        for x, y in zip(rows(pool, req), was):
+            assert torch.equal(x, y[keep.long()])
+        with pytest.raises(pkv.PkvError):
+            req.truncate(24)
+        req.compact(torch.empty(0, dtype=torch.int32, device="cuda"))
+        assert req.length == 0 and req.page_table() == []
+        req.begin_token()
+        req.abort_token()
+        assert pool.check_device_status() == 0
+    finally:
+        pool.close()
+
+
+def test_compact_position_outside_the_length_is_reported():
+    pool = pkv.Pool(1, 8, 2, 64, 16, "f32", 64)
+    try:
+        req = grown(pool, 20)
+        req.compact(torch.tensor([0, 20], dtype=torch.int32, device="cuda"))
+        assert pool.device_status_bits() == pkv.PKV_DEVERR_SEQ_LEN and req.length == 2
+    finally:
+        pool.close()
+
+
+def test_calls_that_cannot_lease_change_nothing():
+    pool = pkv.Pool(1, 6, 2, 64, 16, "bf16", 64)
+    try:
+        req = grown(pool, 40)
+        table, free = req.page_table(), pool.free_list()
+        keep = torch.arange(33, dtype=torch.int32, device="cuda")
+
+        def refused(call):
+            with pytest.raises(pkv.PkvError) as e:
+                call()
+            assert e.value.status == pkv.PKV_ERR_OUT_OF_PAGES
+            assert req.page_table() == table and pool.free_list() == free and req.length == 40
+            assert [pool.page_refs(p) for p in table] == [1] * 3
+
+        refused(lambda: req.fork_batch(4))              # 3 free
+        for n in (1, 3):
+            pool.inject_fault(pkv.PKV_INJECT_LEASE, n)
+            refused(lambda: req.fork_batch(3))
+            pool.inject_fault(pkv.PKV_INJECT_LEASE, n)
+            refused(lambda: req.compact(keep))
+        req.lease_pages(1)
+        table, free = req.page_table(), pool.free_list()
+        with pytest.raises(pkv.PkvError):
+            req.compact(keep)
+        assert req.page_table() == table and pool.free_list() == free
+        kids = req.fork_batch(2)
+        assert all(k.page_table()[:2] == table[:2] and len(k.page_table()) == 3 for k in kids)
+    finally:
+        pool.close()
