@@ -41,11 +41,13 @@
 //
 // Bound: the tensor cores at d_h = 128 (3250 cycles a key tile for 2560 of MMAs at their
 // nominal rate; beside that about 20000 cycles a CTA for its first copies and its
-// output); at 64 the tensor cores and the exponentials about alike.  P V runs twice, for the hi and lo
-// parts of the weights, which carry each to about 2^-17; one bf16 part alone would be
-// off by 2^-9.  O accumulates
-// inside the tensor cores, whose additions truncate: 5e-6 off the formula at 4096
-// positions, 2e-5 at 16384.
+// output); at 64 the tensor cores and the exponentials about alike.
+//
+// Precision.  P V runs twice, for the hi and lo parts of the weights, which carry each to
+// about 2^-17 (one bf16 part alone would be off by 2^-9; for a third TMEM has no columns
+// at d_h = 128): 2e-6 to 3e-6 off the formula.  O accumulates inside the tensor cores,
+// whose additions truncate, which adds up along the cache: 5e-6 at 4096 positions, 2e-5
+// at 16384.
 //
 // Faults: bad lengths and page ids set bits of the device error word (a bad page
 // reads as zeros); a wait that runs out sets the timeout bit and ends the CTA's work
