@@ -597,7 +597,7 @@ typedef struct pkv_differential {
 } pkv_differential;
 
 /* Device scratch bytes that pkv_paged_differential_decode needs (0 for an empty
- * batch, and for a single short request, which runs unsplit). */
+ * batch, and for a few short requests, whose heads a CTA each serves). */
 int pkv_differential_workspace_size(const pkv_pool* pool, int batch, int64_t max_seq_len, size_t* bytes);
 
 /*
@@ -611,8 +611,9 @@ int pkv_differential_workspace_size(const pkv_pool* pool, int batch, int64_t max
  * Both maps are taken in one pass: every K and V row is read once per KV pair.
  * Results do not depend on the order in which the GPU runs the work.  Bad lengths
  * or page ids set the pool's error word; the affected rows of `out` are then
- * unspecified.  Enqueues two kernels on `stream` (split, merge; a single short
- * request the first only) and returns without waiting; calls whose device work can overlap must use different workspaces.
+ * unspecified.  Enqueues two kernels on `stream` (split, merge; a few short
+ * requests the first only) and returns without waiting; calls whose device work
+ * can overlap must use different workspaces.
  */
 int pkv_paged_differential_decode(pkv_pool* pool, int layer, int batch, const float* q,
                                   const void* k_new, const void* v_new, const int32_t* page_tables,

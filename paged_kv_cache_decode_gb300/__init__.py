@@ -382,12 +382,14 @@ class Pool:
         oshape = (B, HQ // 2, 2 * D)
         if out is None:
             out = torch.empty(oshape, dtype=torch.float32, device=q.device)
-            _used_on(out, stream)
+            if stream is not None:
+                _used_on(out, stream)
         if workspace is None:
             n = self._ws_bytes.get((B, max_seq_len))
             if n is None:
                 n = self._ws_bytes[(B, max_seq_len)] = self.differential_workspace_size(B, max_seq_len)
-            workspace = _scratch(n, q.device, stream)
+            if n:
+                workspace = _scratch(n, q.device, stream)
         if page_tables.dim() != 2 or page_tables.shape[0] != B:
             raise ValueError("page_tables must be [batch, max_pages]")
         check(lib.pkv_paged_differential_decode(

@@ -24,8 +24,8 @@
 // dependent, joins them in worker order (no atomics: the same bits every time):
 //     o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s.
 //
-// A single short request instead gives each lane to the warps of one CTA, which join it
-// in shared memory: one launch, no scratch.
+// A few short requests instead give each lane to the warps of one CTA, which join it in
+// shared memory: one launch, no scratch.
 //
 // Three engines take the tiles: bf16 at head width 64 and 128 on mma.sync, fp32 at the
 // same widths on packed fp32 FMAs, every other width on a plain CUDA-core loop.
@@ -90,8 +90,8 @@ struct DfParams {
     int normalise;
     float norm_eps, out_scale;
     float* out;                 // [token][Hp * G][2 D]
-    int alone;                  // > 0: one request, each lane split over this many warps of a
-                                //   CTA that join it in shared memory (no rec, no partials)
+    int alone;                  // > 0: a CTA for each lane, split over this many of its warps,
+                                //   which join it in shared memory (no rec, no partials)
     int4* rec;                  // [W] lane that starts in worker w and ends after it:
                                 //   (request, pair * subs + sub, last worker, 1), or w = 0
     float2* part_ml;            // [2 W][R][2]
@@ -303,15 +303,6 @@ struct Share {
 __device__ __forceinline__ Share share_of(const DfParams& p, int64_t requests_units, int w) {
     Share s;
     s.all = (int64_t)p.Hp * p.subs * requests_units;
-    if (p.alone) {                              // warp w % alone of lane w / alone
-        const int n = requests_units > 0 ? (int)requests_units - kLaneCost : 0;
-        const int lane = w / p.alone, j = w - lane * p.alone;
-        const int64_t first = lane * requests_units + kLaneCost;
-        s.workers = p.W;
-        s.begin = first + j * n / p.alone;
-        s.end = first + (j + 1) * n / p.alone;
-        return s;
-    }
     s.workers = (int)(s.all < p.W ? s.all : p.W);
     s.begin = s.end = 0;
     if (w >= s.workers) return s;
@@ -337,8 +328,7 @@ __device__ __forceinline__ void zero_empty(const DfParams& p, int D) {
     const int n = p.Hp * p.G * 2 * D;
     for (int x = blockIdx.x; x < p.B; x += gridDim.x) {
         if (tiles_at(p, x) > 0) continue;
-        const int threads = p.alone ? 32 * p.alone : blockDim.x;
-        for (int i = threadIdx.x; i < n; i += threads) p.out[(int64_t)x * n + i] = 0.f;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) p.out[(int64_t)x * n + i] = 0.f;
     }
 }
 
@@ -384,6 +374,34 @@ __device__ __forceinline__ bool row_at(const DfParams& p, const LaneRows& L, int
 // Fetch a tensor map into the descriptor cache.
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// A CTA that has one lane (p.alone): this warp's tiles of it as share and cursor.  Returns
+// the lane's tiles; 0: an empty slot (its rows are zeros) or a refused length.
+__device__ __forceinline__ int alone_start(const DfParams& p, int D, int warp, Share& share, Cursor& c) {
+    const int LN = p.Hp * p.subs;
+    c.x = blockIdx.x / LN;
+    c.ln = blockIdx.x - c.x * LN;
+    c.h = c.ln / p.subs;
+    c.sub = c.ln - c.h * p.subs;
+    cursor_load(p, c);
+    if (c.ln == 0 && threadIdx.x == 0 && !len_ok(p, len_at(p, c.x))) atomicOr(p.err, PKV_DEVERR_SEQ_LEN);
+    share.all = share.workers = 0;
+    share.begin = warp * c.n / p.alone;
+    share.end = (warp + 1) * c.n / p.alone;
+    if (c.n == 0) {
+        const LaneRows L = lane_rows(p, c.x, c.h, c.sub);
+        for (int r = warp; r < p.R; r += p.alone) {
+            int64_t row;
+            int head, st, en;
+            if (!row_at(p, L, r, row, head, st, en)) continue;
+            for (int i = threadIdx.x & 31; i < 2 * D; i += 32) p.out[row * 2 * D + i] = 0.f;
+        }
+    }
+    c.tile = (int)share.begin;
+    c.f = share.begin < share.end ? share.begin : share.end;
+    cursor_place(p, c);
+    return c.n;
 }
 
 // A warp, a few tiles ahead: fetch into L1 the queries that the lane at `c` starts with, or
@@ -435,9 +453,9 @@ __device__ __forceinline__ void store_row(const DfParams& p, int64_t row, const 
     }
 }
 
-// One request whose lanes are each split over p.alone warps of one CTA: after the warps'
-// pieces, their partials are joined in shared memory.  A warp's partial lies in its own
-// part of the ring (its tiles are used up): (m, l) [R][2], then o [R][2][2 D].
+// A lane split over p.alone warps of one CTA: after the warps' pieces, their partials are
+// joined in shared memory.  A warp's partial lies in its own part of the ring (its tiles
+// are used up): (m, l) [R][2], then o [R][2][2 D].
 constexpr int kPartOffset = 128;
 
 template <int D, int R>
@@ -447,8 +465,8 @@ __device__ __forceinline__ void join_alone(const DfParams& p, unsigned char* sme
     if (!worked && lane < 2 * R)
         reinterpret_cast<float2*>(smem + warp * warp_bytes)[lane] = make_float2(-INFINITY, 0.f);
     asm volatile("bar.sync 2, %0;" ::"r"(32 * p.alone) : "memory");
-    const int ln = blockIdx.x, h = ln / p.subs;
-    const LaneRows L = lane_rows(p, 0, h, ln - h * p.subs);
+    const int LN = p.Hp * p.subs, req = blockIdx.x / LN, ln = blockIdx.x - req * LN, h = ln / p.subs;
+    const LaneRows L = lane_rows(p, req, h, ln - h * p.subs);
     for (int r = warp; r < R; r += p.alone) {
         int64_t row;
         int head, st, en;
@@ -580,7 +598,7 @@ differential_core_kernel(const __grid_constant__ DfParams p) {
     if (lane == 0 && w < p.W) {
         for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
         fence_mbar_init();
-        if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
+        p.rec[w] = make_int4(0, 0, 0, 0);
     }
     int stride, entries;
     const int64_t total = build_prefix(p, prefix, stride, entries);
@@ -904,15 +922,21 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
         fence_mbar_init();
         if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
     }
-    int stride, entries;
-    const int64_t total = build_prefix(p, prefix, stride, entries);
-    zero_empty(p, D);
-    const Share share = share_of(p, total, w);
-    if (p.alone && total == 0) return;              // an empty slot
+    Share share;
+    Cursor cur;
+    int alone_tiles = 0;
+    if (p.alone) {
+        alone_tiles = alone_start(p, D, warp, share, cur);
+        if (alone_tiles == 0) return;
+    } else {
+        int stride, entries;
+        const int64_t total = build_prefix(p, prefix, stride, entries);
+        zero_empty(p, D);
+        share = share_of(p, total, w);
+        if (share.begin == share.end) return;
+        cur = cursor_at(p, prefix, stride, entries, share.begin);
+    }
     const bool worked = share.begin < share.end;
-    if (!worked && !p.alone) return;
-    Cursor cur = cursor_at(p, prefix, stride, entries, worked ? share.begin : 0);
-    if (!worked) cur.f = share.end;
     Cursor prod = cur;
     Pager pager;
     const uint64_t policy = l2_stream_policy();
@@ -1189,7 +1213,7 @@ differential_f32_kernel(const __grid_constant__ DfParams p, const __grid_constan
         cursor_next(p, cur);
     }
     // a lane of one tile, or of one warp, is finished already
-    if (p.alone > 1 && total > kLaneCost + 1)
+    if (p.alone > 1 && alone_tiles > 1)
         join_alone<D, R>(p, smem, M::STAGES * M::STAGE_BYTES, warp, worked);
 }
 
@@ -1301,15 +1325,21 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
         fence_mbar_init();
         if (!p.alone) p.rec[w] = make_int4(0, 0, 0, 0);
     }
-    int stride, entries;
-    const int64_t total = build_prefix(p, prefix, stride, entries);
-    zero_empty(p, D);
-    const Share share = share_of(p, total, w);
-    if (p.alone && total == 0) return;              // an empty slot
+    Share share;
+    Cursor cur;
+    int alone_tiles = 0;
+    if (p.alone) {
+        alone_tiles = alone_start(p, D, warp, share, cur);
+        if (alone_tiles == 0) return;
+    } else {
+        int stride, entries;
+        const int64_t total = build_prefix(p, prefix, stride, entries);
+        zero_empty(p, D);
+        share = share_of(p, total, w);
+        if (share.begin == share.end) return;
+        cur = cursor_at(p, prefix, stride, entries, share.begin);
+    }
     const bool worked = share.begin < share.end;
-    if (!worked && !p.alone) return;
-    Cursor cur = cursor_at(p, prefix, stride, entries, worked ? share.begin : 0);
-    if (!worked) cur.f = share.end;
     Cursor prod = cur;
     Pager pager;
     const uint64_t policy = l2_stream_policy();
@@ -1672,7 +1702,7 @@ differential_mma_kernel(const __grid_constant__ DfParams p, const __grid_constan
         cursor_next(p, cur);
     }
     // a lane of one tile, or of one warp, is finished already
-    if (p.alone > 1 && total > kLaneCost + 1)
+    if (p.alone > 1 && alone_tiles > 1)
         join_alone<D, R>(p, smem, M::STAGES * M::STAGE_BYTES, warp, worked);
 }
 
@@ -1995,11 +2025,15 @@ cudaError_t launch_f32(const DfParams& p, const void* tmap_k, const void* tmap_v
     return cudaGetLastError();
 }
 
-// A single request of up to kAloneTiles tiles a warp gives each lane to the warps of one
-// CTA, which join it in shared memory: one launch, no scratch.  One token on the device,
-// against the split over the GPU and its merge: 12 heads of 64, fp32, 128 / 256 positions
-// 9.6 / 11.2 us against 10.5 / 11.6; 8 heads of 128, bf16, 128 / 256 positions 12.8 / 14.2
-// against 14.1 / 14.8; at 512 positions the split wins (12.7 against 15.0; 17.3, 17.5).
+// A decode of up to kAloneTiles tiles a warp, and no more lanes than SMs, gives each lane to
+// the warps of one CTA, which join it in shared memory: one launch, no scan of the lengths,
+// no scratch.  On the device, against the split over the GPU and its merge, at 128 / 256
+// positions a request: 12 heads of 64, fp32, 1 request 8.2 / 9.7 us against 10.5 / 11.6, 8
+// requests 10.0 / 11.4 against 14.1 / 14.9, 24 requests 10.3 / 12.2 against 14.9 / 16.7; 8
+// heads of 128, bf16, 1 request 11.6 / 13.0 against 14.1 / 14.8, 8 requests 13.3 / 14.7
+// against 17.6 / 18.5, 36 requests 13.5 / 15.4 against 18.5 / 20.1.  At 512 positions the
+// split wins for one request (12.7 against 15.0; 17.3, 17.5).
+// Both forms are one kernel: as two, both were within 2 % of this, for a third more to compile.
 constexpr int kAloneTiles = 4;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -2038,12 +2072,12 @@ int warps_of(int dtype, int D, int rows) {
 
 }  // namespace
 
-DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, int64_t requests, int64_t lanes,
+DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, bool decode, int64_t lanes,
                                      int64_t max_len) {
     const int warps = warps_of(dtype, D, rows), tile = tile_of(dtype, D);
     const int64_t per = (max_len + tile - 1) / tile, tiles = lanes * per;
     DifferentialSplit s{};
-    if (requests == 1 && (D == 64 || D == 128) && per <= (int64_t)kAloneTiles * warps && lanes <= num_sms) {
+    if (decode && (D == 64 || D == 128) && per <= (int64_t)kAloneTiles * warps && lanes <= num_sms) {
         s.alone = per < warps ? (int)per : warps;
         s.workers = (int)lanes * s.alone;
         return s;

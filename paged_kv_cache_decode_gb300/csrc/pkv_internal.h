@@ -264,7 +264,7 @@ cudaError_t launch_shared_prefix_hook(const void* ctx, cudaStream_t stream);
 // ------------------------------------------------ differential attention --
 
 // How a launch splits its lanes: over `workers` warps of the GPU, joined by a merge kernel
-// through scratch; or (one short request, alone > 0) each over `alone` warps of one CTA.
+// through scratch; or (few short lanes, alone > 0) each over `alone` warps of one CTA.
 struct DifferentialSplit {
     int workers, alone;
 };
@@ -327,9 +327,9 @@ int differential_rows(int dtype, int D, int G);
 // Chunk tokens of one lane of a prefill through lanes.
 int differential_block_tokens(int dtype, int D, int G);
 
-// Workers of one launch over `lanes` lanes, of all requests, of at most max_len attended
-// positions.
-DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, int64_t requests, int64_t lanes,
+// The split of one launch over `lanes` lanes, of all requests, of at most max_len attended
+// positions.  decode: not a prefill through lanes.
+DifferentialSplit differential_split(int dtype, int D, int rows, int num_sms, bool decode, int64_t lanes,
                                      int64_t max_len);
 
 DifferentialLayout differential_layout(int D, int rows, DifferentialSplit split);

@@ -279,15 +279,15 @@ int diff_rows(const pkv_pool* p) { return pkv::differential_rows(p->dtype, p->he
 int64_t diff_subs(const pkv_pool* p) { return (p->group + diff_rows(p) - 1) / diff_rows(p); }
 
 // A launch over requests (or chunk blocks) of at most `rows` query rows a lane.
-pkv::DifferentialSplit diff_split(const pkv_pool* p, int64_t requests, int64_t max_seq_len, int rows,
-                                  int64_t subs) {
-    return pkv::differential_split(p->dtype, p->head_dim, rows, p->sms, requests,
+pkv::DifferentialSplit diff_split(const pkv_pool* p, bool decode, int64_t requests, int64_t max_seq_len,
+                                  int rows, int64_t subs) {
+    return pkv::differential_split(p->dtype, p->head_dim, rows, p->sms, decode,
                                    requests * (p->heads / 2) * subs,
                                    pkv::attended_len(max_seq_len, p->window));
 }
 
 pkv::DifferentialSplit diff_decode_split(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
-    return diff_split(p, requests, max_seq_len, diff_rows(p), diff_subs(p));
+    return diff_split(p, true, requests, max_seq_len, diff_rows(p), diff_subs(p));
 }
 
 size_t diff_decode_bytes(const pkv_pool* p, int64_t requests, int64_t max_seq_len) {
@@ -308,8 +308,7 @@ int diff_chunk_rows(const pkv_pool* p) {
 
 pkv::DifferentialSplit diff_chunk_split(const pkv_pool* p, int batch, int64_t n) {
     const int64_t rows = diff_chunk_rows(p), all = (int64_t)diff_block_tokens(p) * p->group;
-    // at least two "requests": blocks of chunk tokens are never a single request's decode
-    return diff_split(p, n / diff_block_tokens(p) + batch + 1, p->max_context, (int)rows,
+    return diff_split(p, false, n / diff_block_tokens(p) + batch, p->max_context, (int)rows,
                       (all + rows - 1) / rows);
 }
 

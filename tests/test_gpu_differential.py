@@ -97,6 +97,35 @@ def test_decode_single_requests(dtype, D, G, window):
         checked(Case([t], 2, G, D, dtype=dtype, seed=t, window=window), f"t={t}")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 16), (128, 4)])
+@pytest.mark.parametrize("window", [0, 33])
+def test_decode_few_short_requests(dtype, D, G, window):
+    """Lanes of a CTA each: ragged lengths, empty slots, several row blocks a pair."""
+    checked(Case([1, 0, 16, 17, 100, 0, 184, 5], 4, G, D, dtype=dtype, seed=D + G, window=window))
+    checked(Case([0, 0, 1], 2, G, D, dtype=dtype, seed=D + G, window=window))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decode_few_short_requests_with_bad_entries(dtype):
+    c = Case([30, 60, 5], 2, 2, 64, dtype=dtype, seed=1)
+    try:
+        assert c.pool.differential_workspace_size(3, c.max_len) == 0
+        for bad in (-1, c.max_len + 1):
+            c.dlens[0] = bad
+            c.out.fill_(math.nan)
+            c.run()
+            assert c.pool.device_status_bits() == pkv.PKV_DEVERR_SEQ_LEN
+            assert near(c, 1)
+        c.dlens[0] = 30
+        c.tables[0, 1] = c.pool.pages
+        c.run()
+        assert c.pool.device_status_bits() == pkv.PKV_DEVERR_PAGE_ID
+        assert near(c, 1)
+    finally:
+        c.close()
+
+
 def test_decode_single_request_of_a_bad_length():
     for dtype in ("f32", "bf16"):
         c = Case([40], 2, 1, 64, dtype=dtype)
@@ -487,7 +516,7 @@ def test_prefill_device_refusals():
 
 
 def test_host_refusals():
-    c = Case([30, 300], 2, 1, 64, dtype="bf16")        # two requests: scratch is needed
+    c = Case([30, 3000], 2, 1, 64, dtype="bf16")       # long enough for scratch
     plain = pkv.Pool(1, 4, 2, 64, 16, "bf16", 64)
     try:
         args = (0, c.q, c.k_new, c.v_new, c.tables, c.dlens, c.max_len)
